@@ -354,6 +354,108 @@ int tpl_prefill_chunk(tpl_plan *plan, const void *packed, const tpl_kv *kv, cons
                       int32_t T, int64_t start, void *y, float *y32, void *ws, size_t ws_bytes,
                       int32_t reduce_mode, tpl_stream stream);
 
+/* ---- a paged KV cache and ragged batches ---------------------------------
+ *
+ * The calls above keep one contiguous cache row per sequence and give every
+ * sequence of a call the same length.  The calls below keep the keys in pages
+ * that a table names per sequence, so sequences of different lengths share
+ * one pool and one call.  A decode step is tpl_paged_append, then
+ * tpl_paged_attn, between the projections tpl_qkv (on a plan without
+ * TPL_ROPE; its own cache argument may be one scratch slot, S = 0) and
+ * tpl_o_proj.  The pages describe neither; both follow the ownership rule of
+ * "Tensor parallel scaling curves", "What tensor parallelism actually
+ * splits": a shard's pages hold the heads it owns.
+ *
+ * What the device arrays say is checked by the kernels: a page id, a length
+ * or a start outside its range sets the device error word
+ * (tpl_last_device_error returns TPL_EDEVICE), reads page 0 in its place or
+ * skips the write, and never leaves the buffers; that sequence's results are
+ * then not to be used. */
+
+#define TPL_BF16 0
+#define TPL_F32 1
+
+/* The pool of one layer, bf16, shard-major:
+ *   k, v: [t][n_pages][n_kv/t][page_size][head_dim], 16-byte aligned.
+ * page_size is 16, 32, 64, 128 or 256 (other values: TPL_EUNSUPPORTED), and
+ * n_kv * n_pages * page_size is below 2^31. */
+typedef struct {
+    void *k, *v;
+    int32_t n_pages, page_size;
+} tpl_paged_kv;
+
+/* A batch of sequences (device arrays, int32; nothing is read of them on the
+ * host, so a captured call follows their contents).  Position p of sequence b
+ * lives in page page_table[b * table_stride + p / page_size], slot p %
+ * page_size.  kv_len[b] counts the sequence's keys, this call's tokens
+ * included.  q_start[n_seqs + 1] says where the tokens lie in the rows of q
+ * (sequence b has rows q_start[b] .. q_start[b + 1] - 1, in ascending order; rows
+ * from q_start[n_seqs] on are left as they were); the last of them is at
+ * position kv_len[b] - 1.  q_start == NULL: one token per sequence, row b is
+ * sequence b, and n_tokens == n_seqs.  A token whose position is below 0 is
+ * inactive (kv_len[b] == 0 pads a batch): it is not appended and sees no key.
+ * At most 1024 sequences and 2^22 rows, and max_pages * page_size below
+ * 2^31 - 4096 (TPL_EUNSUPPORTED). */
+typedef struct {
+    const int32_t *page_table;
+    int64_t table_stride; /* entries between the rows of the table           */
+    int32_t max_pages;    /* entries of a row that may be read               */
+    int32_t n_seqs;
+    const int32_t *kv_len;
+    const int32_t *q_start;
+    int32_t n_tokens;     /* rows of q, k, v and of the outputs              */
+} tpl_paged_batch;
+
+/* Rows of heads: element (token, head, e) of head_dim contiguous values at
+ * data[token * token_stride + head * head_stride + e]; type TPL_BF16 or
+ * TPL_F32.  data and both strides are multiples of 16 bytes, so a slice of a
+ * fused projection's output can be given as it is. */
+typedef struct {
+    void *data;
+    int32_t type;
+    int64_t token_stride, head_stride; /* in elements */
+} tpl_heads;
+
+/* Workspace of the paged attention calls for up to n_seqs sequences and
+ * n_tokens rows.  Zero it once with tpl_workspace_init; two calls that may
+ * overlap on the GPU (other streams, two captured graphs) need one each. */
+int tpl_paged_workspace_size(const tpl_plan *plan, int32_t n_seqs, int32_t n_tokens, size_t *out);
+
+/* Append this call's tokens: k and v [n_tokens][n_kv] are rounded to bf16 into
+ * their slots, with TPL_ROPE k turned to its position first (the rotation of
+ * tpl_dims), and q [n_tokens][n_q] turned the same way into q_out (q and
+ * q_out both NULL: no q; q_out may be q itself, and must not overlap it
+ * otherwise).  All four have the same type.  Two tokens must not share a
+ * slot. */
+int tpl_paged_append(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,
+                     const tpl_heads *q_out, const tpl_heads *k, const tpl_heads *v, tpl_stream stream);
+
+/* Owned-head attention over the pages.  The token at position p sees the keys
+ * j <= p with j > p - window (window = 0: no limit) or j < sinks (the first
+ * tokens that stay visible behind a window).  A page none of whose keys is
+ * seen is not read, nor is its table entry.  o: [n_tokens][n_q * d], the activation
+ * type; lse: fp32 [n_tokens][n_q] or NULL, the natural logarithm of the
+ * softmax denominator.  A token that sees no key gets o = 0, lse = -inf.
+ * Logits are q.k / sqrt(d); q is TPL_F32 or TPL_BF16 (fp32 queries cost the
+ * prompts a second product).  With q_start (prompts) a plan with
+ * TPL_FP32_WEIGHTS is TPL_EUNSUPPORTED, as in prefill.  The same inputs give
+ * the same bits. */
+int tpl_paged_attn(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,
+                   int32_t window, int32_t sinks, void *o, float *lse, void *ws, size_t ws_bytes, tpl_stream stream);
+
+/* The same without a window, for a decode batch (q_start NULL) whose
+ * sequences begin with the same shared_len keys: the first shared_len /
+ * page_size entries of every row of the table name the same pages, and only
+ * row 0's are read, once for the whole batch, on the tensor cores.
+ * shared_len is a multiple of page_size and at most max_pages * page_size
+ * (TPL_EINVAL); 0 is tpl_paged_attn.  kv_len counts the shared keys; a
+ * sequence may end inside them.  TPL_EUNSUPPORTED with q_start (prompts that
+ * share pages read them from L2 in tpl_paged_attn) and with
+ * TPL_FP32_WEIGHTS. */
+int tpl_paged_attn_shared(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_paged_batch *batch,
+                          int64_t shared_len, const tpl_heads *q, void *o, float *lse, void *ws, size_t ws_bytes,
+                          tpl_stream stream);
+
 /* ---- the individual steps (each is one kernel launch, except where noted;
  *      the decode calls above are these in order) --------------------------- */
 

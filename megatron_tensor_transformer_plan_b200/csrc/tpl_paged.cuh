@@ -1,0 +1,236 @@
+// What the paged-cache kernels share: the view of a ragged batch over the
+// pages, with the bounds checks of everything the device arrays say (a page
+// id, length or start outside its range is recorded in the error word and
+// replaced by one that is in bounds), and the append.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "tpl_common.cuh"
+#include "tpl_internal.h"
+
+namespace tpl {
+
+constexpr unsigned kErrPaged = 32u;  // error word: a page id, length or start out of range
+
+struct PagedView {
+    const int32_t *table;     // [n_seqs][max_pages], rows table_stride apart
+    int64_t table_stride;
+    const int32_t *kv_len;    // [n_seqs]
+    const int32_t *q_start;   // [n_seqs + 1], or NULL: one token per sequence
+    int32_t max_pages, n_pages, page_shift, n_seqs, n_tokens, nkv, nkv_s;
+};
+
+// Keys of sequence b.
+__device__ __forceinline__ int paged_len(const PagedView &v, int b) {
+    const int len = v.kv_len[b];
+    const int64_t cap = (int64_t)v.max_pages << v.page_shift;
+    if (len < 0 || len > cap) {
+        record_error(kErrPaged);
+        return 0;
+    }
+    return len;
+}
+
+// First token row and token count of sequence b.
+__device__ __forceinline__ void paged_tokens(const PagedView &v, int b, int &start, int &count) {
+    if (!v.q_start) {
+        start = b;
+        count = 1;
+        return;
+    }
+    const int s = v.q_start[b], e = v.q_start[b + 1];
+    if (s < 0 || e < s || e > v.n_tokens) {
+        record_error(kErrPaged);
+        start = count = 0;
+        return;
+    }
+    start = s;
+    count = e - s;
+}
+
+// The pool row (128 values) of page entry `entry` of sequence b for global kv
+// head j, slot 0; -1 when the table names a page that is not there.
+__device__ __forceinline__ int64_t paged_row(const PagedView &v, int b, int entry, int j) {
+    const int page = v.table[b * v.table_stride + entry];
+    if (page < 0 || page >= v.n_pages) {
+        record_error(kErrPaged);
+        return -1;
+    }
+    const int sh = j / v.nkv_s, jl = j % v.nkv_s;
+    return (((int64_t)sh * v.n_pages + page) * v.nkv_s + jl) << v.page_shift;
+}
+
+// ---- append ----------------------------------------------------------------
+//
+// q' = R(p) q, and for the token's slot of the cache K = bf16(R(p) k), V =
+// bf16(v), where R(p) turns the pair (x[e], x[e + 64]) by p * rope_base^(-2e/128)
+// (RoFormer's rotation, half-split pairing; TPL_ROPE) or is the identity.
+// A pass over memory: every value is read once and written once, so HBM is
+// the bound and the rotation has to stay hidden behind the loads.  One CTA
+// takes one token (or a part of its heads when there are few tokens): its 64
+// angles are formed once, in turns and in fp64 (far positions are thousands
+// of turns, of which only the fraction counts), shared by all heads, and
+// evaluated while the CTA's first loads are in flight.  A work item is 16
+// bytes of a row's first half with the 16 bytes of the second half they are
+// turned with.
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendItems = 4;  // items in flight per thread
+
+struct AppendArgs {
+    PagedView v;
+    const void *q, *k, *kv;  // tokens x heads x 128 (kv: the values)
+    void *q_out;             // NULL: no q
+    int64_t q_ts, q_hs, qo_ts, qo_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
+    __nv_bfloat16 *kc, *vc;
+    int nq;                  // query heads (0: no q)
+    int rope;
+    int items_per_cta;
+    double turns[64];        // rope_base^(-2e/128) / (2 pi)
+};
+
+template <typename T>
+struct AppendIo;
+template <>
+struct AppendIo<float> {
+    static constexpr int N = 4;  // values per 16 bytes
+    static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x);
+        x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z);
+        x[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    static __device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&x)[4]) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    }
+};
+template <>
+struct AppendIo<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16lo(w[i]);
+            x[2 * i + 1] = bf16hi(w[i]);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                          pack_bf16x2(x[6], x[7]));
+    }
+    static __device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&x)[8]) {
+        *reinterpret_cast<uint4 *>(p) = pack(x);
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+    using Io = AppendIo<T>;
+    constexpr int N = Io::N;
+    constexpr int IPH = 64 / N;  // items per head
+    __shared__ float s_cos[64], s_sin[64];
+    __shared__ int s_seq;
+    const int tok = blockIdx.x;
+    const int nkv = a.v.nkv;
+    const int items = (a.nq + 2 * nkv) * IPH;
+    const int i0 = blockIdx.y * a.items_per_cta, i1 = min(items, i0 + a.items_per_cta);
+    if (threadIdx.x == 0) s_seq = -1;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+
+    auto source = [&](int item) -> const uint4 * {
+        const int h = item / IPH, c = item % IPH;
+        const T *p;
+        if (h < a.nq) p = static_cast<const T *>(a.q) + tok * a.q_ts + h * a.q_hs;
+        else if (h < a.nq + nkv) p = static_cast<const T *>(a.k) + tok * a.k_ts + (h - a.nq) * a.k_hs;
+        else p = static_cast<const T *>(a.kv) + tok * a.v_ts + (h - a.nq - nkv) * a.v_hs;
+        return reinterpret_cast<const uint4 *>(p + c * N);
+    };
+    uint4 lo[kAppendItems], hi[kAppendItems];
+#pragma unroll
+    for (int r = 0; r < kAppendItems; ++r) {
+        const int item = i0 + threadIdx.x + r * kAppendThreads;
+        if (item < i1) {
+            const uint4 *p = source(item);
+            lo[r] = p[0];
+            hi[r] = p[4 * sizeof(T)];  // 64 values on
+        }
+    }
+
+    // the token's sequence: every thread looks at some of them
+    if (a.v.q_start) {
+        for (int b = threadIdx.x; b < a.v.n_seqs; b += kAppendThreads)
+            if (a.v.q_start[b] <= tok && tok < a.v.q_start[b + 1]) atomicMax(&s_seq, b);
+    } else if (threadIdx.x == 0) {
+        s_seq = tok;
+    }
+    __syncthreads();
+    const int b = s_seq;
+    if (b < 0) return;  // a row behind the last sequence
+    int start, count;
+    paged_tokens(a.v, b, start, count);
+    const int pos = paged_len(a.v, b) - count + (tok - start);
+    if (count == 0 || pos < 0) return;  // an inactive sequence
+    if (a.rope && threadIdx.x < 64) {
+        const double turn = (double)pos * a.turns[threadIdx.x];
+        float s, c;
+        sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
+        s_cos[threadIdx.x] = c;
+        s_sin[threadIdx.x] = s;
+    }
+    const int slot = pos & ((1 << a.v.page_shift) - 1);
+    const int64_t page_row = paged_row(a.v, b, pos >> a.v.page_shift, 0);  // head 0 of shard 0
+    __syncthreads();
+
+    for (int base = i0 + threadIdx.x; base < i1; base += kAppendItems * kAppendThreads) {
+        if (base != i0 + (int)threadIdx.x) {
+#pragma unroll
+            for (int r = 0; r < kAppendItems; ++r) {
+                const int item = base + r * kAppendThreads;
+                if (item < i1) {
+                    const uint4 *p = source(item);
+                    lo[r] = p[0];
+                    hi[r] = p[4 * sizeof(T)];
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kAppendItems; ++r) {
+            const int item = base + r * kAppendThreads;
+            if (item >= i1) break;
+            const int h = item / IPH, e = (item % IPH) * N;
+            float x[N], y[N];
+            Io::unpack(lo[r], x);
+            Io::unpack(hi[r], y);
+            if (a.rope && h < a.nq + nkv) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float c = s_cos[e + i], s = s_sin[e + i], x0 = x[i];
+                    x[i] = x0 * c - y[i] * s;
+                    y[i] = y[i] * c + x0 * s;
+                }
+            }
+            if (h < a.nq) {
+                T *p = static_cast<T *>(a.q_out) + tok * a.qo_ts + h * a.qo_hs + e;
+                *reinterpret_cast<uint4 *>(p) = Io::pack(x);
+                *reinterpret_cast<uint4 *>(p + 64) = Io::pack(y);
+            } else if (page_row >= 0) {
+                const bool is_k = h < a.nq + nkv;
+                const int j = h - a.nq - (is_k ? 0 : nkv);
+                const int sh = j / a.v.nkv_s, jl = j % a.v.nkv_s;
+                const int64_t row = page_row + ((((int64_t)sh * a.v.n_pages * a.v.nkv_s) + jl) << a.v.page_shift) + slot;
+                __nv_bfloat16 *p = (is_k ? a.kc : a.vc) + row * 128 + e;
+                Io::store_bf16(p, x);
+                Io::store_bf16(p + 64, y);
+            }
+        }
+    }
+}
+
+}  // namespace tpl

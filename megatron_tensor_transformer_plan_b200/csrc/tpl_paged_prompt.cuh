@@ -1,0 +1,780 @@
+// Attention of many query rows over a paged cache, on the 5th-generation
+// tensor cores: the prompts of a ragged batch (causal, with a window and
+// sinks), and the common prefix of a decode batch.
+//
+// A row is one (token, query head); the g heads that share a kv head are rows
+// of the same tile (row = token * g + head), so every key is read once for
+// all of them.  An item is 256 rows of one kv head (two tiles of 128: tensor
+// memory holds S and O of both) against the tiles of 128 keys that any of its
+// rows sees.  The items' key tiles are laid end to end, kv head by kv head, and
+// CTA c of G takes an equal contiguous range of them, so the SMs finish
+// together whatever the lengths are and a few rows against a long cache still
+// fill the GPU.  An item that is cut leaves one partial (max, sum,
+// unnormalised output) per CTA in the workspace; a second kernel joins them.
+// Neighbouring CTAs work on the same kv head, so its keys come from L2.
+//
+// 12 warps:
+//   0     TMA producer: K and V tiles in turn into a ring, a lane per page
+//         part (64 dims of at most 128 keys of one page), no multicast;
+//   1     TMEM owner and MMA issuer (one thread);
+//   2     replaces the values of keys that no row sees by zero (0 * NaN is NaN)
+//         in the tiles that have such keys, before the MMA reads them;
+//   3     idle;
+//   4-7   softmax of tile 0, 8-11 softmax of tile 1: one thread per row.
+// S = Q K^T reads Q (bf16, or bf16 hi + lo when q is fp32: two products) and K
+// from shared memory; P replaces S in tensor memory as bf16; O += P V.  The
+// two tiles alternate, so the MMAs of one run under the softmax of the other.
+// P has one bf16 part: with o rounded to bf16 anyway, the two roundings are of
+// the same size (2^-9 of each term against 2^-9 of the sum); the denominator
+// adds the unrounded fp32 terms.
+// The bound is the larger of the two products on the tensor cores and one
+// exponential per (row, key): 128 x 128 of them take the SM's 16 lanes of the
+// special-function unit as long as the two products take.
+//
+// Every wait is bounded (2 s); on a timeout the roles stop, the error word is
+// set, copies in flight are waited for (bounded) and TMEM is released.
+#pragma once
+
+#include <cuda.h>
+
+#include "tpl_attn_tc.cuh"
+#include "tpl_paged.cuh"
+
+namespace tpl {
+
+constexpr int kPtKeys = 128;                   // keys per tile
+constexpr int kPtHalf = kPtKeys * 128;         // 128 rows x 64 dims, bf16: 16 KB
+constexpr int kPtTile = 2 * kPtHalf;           // one K, V or Q tile: 32 KB
+constexpr int kPtThreads = 384;
+constexpr int kPtMinTiles = 2;                 // key tiles per CTA at least
+constexpr uint32_t kPtO = 0, kPtS = 256;       // TMEM columns: O of tile t at 128 t, S at 256 + 128 t
+
+template <bool QF32>
+struct PtSmem {
+    static constexpr int QPARTS = QF32 ? 2 : 1;
+    static constexpr int NST = QF32 ? 3 : 5;   // ring stages of one tile; odd: see v_ready
+    static constexpr int Q = 2 * QPARTS * kPtTile;
+    static constexpr int BAR = 1536;
+    static constexpr size_t BYTES = (size_t)Q + NST * kPtTile + BAR + 1024;
+    static_assert(BYTES <= 232448, "shared memory per block");
+    static_assert(NST % 2 == 1, "K and V alternate on every stage");
+};
+
+struct PagedPromptArgs {
+    CUtensorMap tm_k, tm_v;  // pool rows x 128, boxes of 64 dims x min(128, page) rows
+    PagedView v;
+    const void *q;           // [n_tokens] rows
+    int64_t q_ts, q_hs;
+    int nq, g, tb;           // tb = tokens per tile = 128 / g
+    int window, sinks;
+    int shared;              // > 0: the common prefix of this many keys (rows = sequences)
+    float scale_log2;
+    __nv_bfloat16 *o;        // [n_tokens][nq * 128]
+    float *lse;              // [n_tokens][nq] or NULL
+    // partials: slots of rows x 128 floats and rows x 2; prompts: slot 2 c + (not the
+    // CTA's first segment); prefix: slot item + c
+    float *part_o, *part_ml;
+    int part_rows;           // rows per slot
+    int4 *cut;               // [grid] prompts: {first token, row tokens, kv head, parts} of the item CTA c is the first of
+};
+
+// One item: 2 * tb tokens of a sequence against the key tiles they see.
+struct PtItem {
+    int row0, ntok;      // first row of q, tokens
+    int p0;              // position of the first token
+    int len, lo, sk;     // some row sees key j: j < len && (j >= lo || j < sk)
+    int nst, ft, ntk;    // key tiles: 0 .. nst-1, then ft ..; ntk of them
+    __device__ __forceinline__ int tile(int i) const { return i < nst ? i : ft + i - nst; }
+};
+
+__device__ __forceinline__ int pt_items(const PagedPromptArgs &a, int count) { return (count + 2 * a.tb - 1) / (2 * a.tb); }
+
+// The first key of position p's window (p may lie below 0).
+__device__ __forceinline__ int pt_window(const PagedPromptArgs &a, int p) {
+    return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
+__device__ __forceinline__ PtItem pt_item(const PagedPromptArgs &a, int b, int start, int count, int it) {
+    PtItem x;
+    const int t0 = it * 2 * a.tb;
+    x.row0 = start + t0;
+    x.ntok = min(2 * a.tb, count - t0);
+    if (a.shared > 0) {
+        x.p0 = a.shared;
+        x.len = a.shared;
+        x.lo = x.sk = x.nst = x.ft = 0;
+        x.ntk = (a.shared + kPtKeys - 1) / kPtKeys;
+        return x;
+    }
+    x.p0 = paged_len(a.v, b) - count + t0;
+    x.len = max(0, x.p0 + x.ntok);
+    x.lo = pt_window(a, x.p0);
+    x.sk = min(a.sinks, x.lo);
+    x.nst = (x.sk + kPtKeys - 1) / kPtKeys;
+    x.ft = max(x.lo / kPtKeys, x.nst);
+    // rows that see no key still take one (masked) tile, which gives them zeros
+    x.ntk = max(1, x.nst + max(0, (int)(((int64_t)x.len + kPtKeys - 1) / kPtKeys) - x.ft));
+    return x;
+}
+
+// Walks a CTA's segments in order; every role walks on its own.
+struct PtWalk {
+    int64_t u, u1;
+    int j, b, it;        // kv head, sequence, item of the sequence
+    int start, count;    // its tokens
+    int done;            // key tiles of the item before u
+    int idx;             // items before this one, over all kv heads (prefix mode)
+    PtItem x;
+    int i0, n;           // this segment: key tiles i0 .. i0 + n - 1 of the item
+    bool first;          // the CTA's first segment
+
+    __device__ __forceinline__ void open(const PagedPromptArgs &a) {
+        x = pt_item(a, b, start, count, it);
+        i0 = done;
+        n = (int)min((int64_t)(x.ntk - done), u1 - u);
+    }
+    __device__ __forceinline__ void tokens(const PagedPromptArgs &a) {
+        if (a.shared > 0) {
+            start = 0;
+            count = a.v.n_tokens;
+        } else {
+            paged_tokens(a.v, b, start, count);
+        }
+    }
+    __device__ __forceinline__ bool next(const PagedPromptArgs &a) {
+        u += n;
+        if (u >= u1) return false;
+        first = false;
+        done = 0;
+        ++idx;
+        if (++it == pt_items(a, count)) {
+            it = 0;
+            const int ns = a.shared > 0 ? 1 : a.v.n_seqs;
+            do {
+                if (++b == ns) {
+                    b = 0;
+                    ++j;
+                }
+                tokens(a);
+            } while (count == 0);
+        }
+        open(a);
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return i0 == 0 && n == x.ntk; }
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 2^x by the special-function unit (relative error 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+template <bool QF32>
+__global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __grid_constant__ PagedPromptArgs a) {
+    using SM = PtSmem<QF32>;
+    constexpr int NST = SM::NST;
+    extern __shared__ __align__(1024) unsigned char pt_raw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)pt_raw + 1023) & ~(uintptr_t)1023);
+    unsigned char *s_q = sm;              // [tile][part][half][128 rows][128 B]
+    unsigned char *ring = sm + SM::Q;
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + NST * kPtTile);  // [NST] tile landed
+    uint64_t *empty = full + NST;         // [NST] tile read by its last MMA
+    uint64_t *v_ready = empty + NST;      // [NST] V tile checked
+    uint64_t *q_ready = v_ready + NST;    // [2]
+    uint64_t *s_full = q_ready + 2;       // [2]
+    uint64_t *p_full = s_full + 2;        // [2]
+    uint64_t *o_full = p_full + 2;        // [2]
+    uint64_t *o_empty = o_full + 2;       // [2]
+    uint64_t *fin = o_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
+    volatile int *s_fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *s_issued = const_cast<int *>(s_fail) + 1;
+    int *s_where = s_issued + 1;          // [4] start of this CTA's range: j, b, item, tiles before
+    long long *s_sum = reinterpret_cast<long long *>((reinterpret_cast<uintptr_t>(s_where + 4) + 7) & ~(uintptr_t)7);
+    static_assert((3 * NST + 11) * 8 + 32 + 16 + 16 * 8 <= SM::BAR, "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&v_ready[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_ready[t], 4);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_full[t], 1);
+            mbar_init(&o_empty[t], 4);
+        }
+        mbar_init(fin, 1);
+        *s_fail = 0;
+        *s_issued = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's range of the key tiles: each thread sums a run of items ----
+    int64_t U1;  // key tiles of one kv head
+    {
+        int *s_item = reinterpret_cast<int *>(ring);  // [n_seqs + 1] items before sequence b
+        const int ns = a.shared > 0 ? 1 : a.v.n_seqs;
+        constexpr int PT = (kPagedMaxSeqs + kPtThreads - 1) / kPtThreads;
+        const int per = (ns + kPtThreads - 1) / kPtThreads;
+        int mine[PT], cnt = 0;
+#pragma unroll
+        for (int x = 0; x < PT; ++x) {
+            const int b = threadIdx.x * per + x;
+            mine[x] = 0;
+            if (x < per && b < ns) {
+                int start = 0, count = a.v.n_tokens;
+                if (a.shared == 0) paged_tokens(a.v, b, start, count);
+                mine[x] = pt_items(a, count);
+            }
+            cnt += mine[x];
+        }
+        auto scan = [&](long long val) -> long long {  // exclusive prefix over the CTA's threads
+            long long inc = val;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += t;
+            }
+            if (lane == 31) s_sum[warp] = inc;
+            __syncthreads();
+            long long at = inc - val;
+            for (int w = 0; w < warp; ++w) at += s_sum[w];
+            return at;
+        };
+        int at = (int)scan(cnt);
+#pragma unroll
+        for (int x = 0; x < PT; ++x) {
+            const int b = threadIdx.x * per + x;
+            if (x < per && b < ns) {
+                s_item[b] = at;
+                at += mine[x];
+                if (b == ns - 1) s_item[ns] = at;
+            }
+        }
+        __syncthreads();
+        const int items = s_item[ns];
+        const int run = (items + kPtThreads - 1) / kPtThreads;
+        const int k0 = min(items, (int)threadIdx.x * run), k1 = min(items, k0 + run);
+        // items k0 .. k1 - 1: their sequence, then their key tiles
+        auto walk = [&](auto &&visit) {
+            if (k0 >= k1) return;
+            int l = 0, r = ns - 1;  // the last sequence that begins at or before item k0
+            while (l < r) {
+                const int mid = (l + r + 1) >> 1;
+                if (s_item[mid] <= k0) l = mid;
+                else r = mid - 1;
+            }
+            int b = l, start = 0, count = a.v.n_tokens;
+            if (a.shared == 0) paged_tokens(a.v, b, start, count);
+            for (int k = k0; k < k1; ++k) {
+                while (k >= s_item[b + 1]) {
+                    ++b;
+                    if (a.shared == 0) paged_tokens(a.v, b, start, count);
+                }
+                visit(b, k - s_item[b], pt_item(a, b, start, count, k - s_item[b]).ntk);
+            }
+        };
+        long long tiles = 0;
+        walk([&](int, int, int ntk) { tiles += ntk; });
+        long long before = scan(tiles);
+        __syncthreads();
+        if (threadIdx.x == kPtThreads - 1) s_sum[0] = before + tiles;
+        __syncthreads();
+        U1 = s_sum[0];
+        const int64_t U = U1 * a.v.nkv;
+        const int G = (int)min((int64_t)gridDim.x, max((int64_t)1, (U + kPtMinTiles - 1) / kPtMinTiles));
+        if (cta < G && U > 0) {
+            const int64_t u0 = am_start(U, G, cta);
+            const int j = (int)(u0 / U1);
+            const int64_t rel = u0 - j * U1;
+            if (rel >= before && rel < before + tiles) {
+                long long t = before;
+                walk([&](int b, int it, int ntk) {
+                    if (rel >= t && rel < t + ntk) {
+                        s_where[0] = j;
+                        s_where[1] = b;
+                        s_where[2] = it;
+                        s_where[3] = (int)(rel - t);
+                    }
+                    t += ntk;
+                });
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is TMA's from here on
+        __syncthreads();
+    }
+    const int64_t U = U1 * a.v.nkv;
+    const int G = (int)min((int64_t)gridDim.x, max((int64_t)1, (U + kPtMinTiles - 1) / kPtMinTiles));
+    const bool busy = cta < G && U > 0;
+    if (threadIdx.x == 128 && a.cut) a.cut[cta] = make_int4(0, 0, 0, 0);  // the thread that may fill it in below
+
+    PtWalk w;
+    if (busy) {
+        w.u = am_start(U, G, cta);
+        w.u1 = am_start(U, G, cta + 1);
+        w.j = s_where[0];
+        w.b = s_where[1];
+        w.it = s_where[2];
+        w.done = s_where[3];
+        w.first = true;
+        w.tokens(a);
+        w.idx = w.j * pt_items(a, a.v.n_tokens) + w.it;  // (prefix mode: one pseudo sequence)
+        w.open(a);
+    }
+
+    if (busy && warp == 0) {
+        // ---- TMA producer: lane = (dims half, page part) ----
+        const int box_shift = min(a.v.page_shift, 7);
+        const int nsub = kPtKeys >> box_shift;  // at most 8
+        const int half = lane / nsub, sub = lane % nsub;
+        int e = 0;  // ring element: K and V of each tile in turn
+        bool ok = true;
+        do {
+            const PtItem &x = w.x;
+            for (int i = w.i0; ok && i < w.i0 + w.n; ++i) {
+                const int key = x.tile(i) * kPtKeys + (sub << box_shift);
+                const bool want = half < 2 && key < x.len && (key + (1 << box_shift) > x.lo || key < x.sk);
+                int row = 0;
+                if (want) {
+                    const int64_t r = paged_row(a.v, a.shared > 0 ? 0 : w.b, key >> a.v.page_shift, w.j);
+                    row = r < 0 ? 0 : (int)r + (key & ((1 << a.v.page_shift) - 1));
+                }
+                const unsigned bytes = (unsigned)__popc(__ballot_sync(0xffffffffu, want)) << (box_shift + 7);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++e) {
+                    const int s = e % NST;
+                    bool go = true;
+                    if (lane == 0) go = !*s_fail && mbar_wait(&empty[s], ((unsigned)(e / NST) & 1u) ^ 1u);
+                    if (!__all_sync(0xffffffffu, go)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_expect_tx(&full[s], bytes);
+                    __syncwarp();
+                    if (want)
+                        tma_load_2d(ring + s * kPtTile + half * kPtHalf + (sub << (box_shift + 7)),
+                                    kv ? &a.tm_v : &a.tm_k, 64 * half, row, &full[s]);
+                }
+            }
+        } while (ok && w.next(a));
+        if (!ok) *s_fail = 1;
+        if (lane == 0) *s_issued = e;
+    } else if (busy && warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t IDESC_S = umma_idesc(128, kPtKeys);
+            constexpr uint32_t IDESC_PV = umma_idesc(128, 128) | (1u << 16);  // B (V) MN-major
+            int e = 0;                         // ring element of the segment's first K
+            unsigned n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of p_full, and of q_ready / o_empty
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, unsigned parity) {
+                if (ok && (*s_fail || !mbar_wait(bar, parity))) ok = false;
+                return ok;
+            };
+            auto issue_s = [&](int t, int ek) {  // S_t = Q_t K^T
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const unsigned kb = smem_u32(ring + (ek % NST) * kPtTile);
+                const unsigned qb = smem_u32(s_q + t * SM::QPARTS * kPtTile);
+                const uint32_t d = tmem + kPtS + 128u * t;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const unsigned off = (unsigned)((kk >> 2) * kPtHalf + 32 * (kk & 3));
+                    const uint64_t dk = umma_desc(kb + off);
+                    umma(d, umma_desc(qb + off), dk, IDESC_S, kk > 0 ? 1u : 0u);
+                    if (QF32) umma(d, umma_desc(qb + kPtTile + off), dk, IDESC_S, 1u);
+                }
+                umma_commit(&s_full[t]);
+            };
+            auto issue_pv = [&](int t, int ev, bool acc) {  // O_t += P_t V
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const unsigned vb = smem_u32(ring + (ev % NST) * kPtTile);
+                const uint32_t pcol = tmem + kPtS + 128u * t;
+#pragma unroll
+                for (int ks = 0; ks < kPtKeys / 16; ++ks)
+                    umma_ts(tmem + kPtO + 128u * t, pcol + 8 * ks, umma_desc_lbo(vb + 2048 * ks, kPtHalf), IDESC_PV,
+                            (acc || ks > 0) ? 1u : 0u);
+            };
+            do {
+                const int nt = w.x.ntok > a.tb ? 2 : 1;
+                const int n = w.n;
+                for (int t = 0; t < nt && ok; ++t) {
+                    wait(&q_ready[t], n_q[t] & 1u);
+                    if (t == 0) wait(&full[e % NST], (unsigned)(e / NST) & 1u);
+                    if (ok) issue_s(t, e);
+                }
+                if (ok) umma_commit(&empty[e % NST]);
+                for (int i = 0; ok && i < n; ++i) {
+                    const int ek = e + 2 * (i + 1), ev = e + 2 * i + 1;
+                    for (int t = 0; t < nt && ok; ++t) {
+                        if (t == 0) wait(&v_ready[ev % NST], (unsigned)((ev / NST) >> 1) & 1u);
+                        if (i == 0) wait(&o_empty[t], (n_q[t] & 1u) ^ 1u);
+                        wait(&p_full[t], n_p[t] & 1u);
+                        if (!ok) break;
+                        ++n_p[t];
+                        issue_pv(t, ev, i > 0);
+                        if (t == nt - 1) umma_commit(&empty[ev % NST]);
+                        if (i == n - 1) {
+                            umma_commit(&o_full[t]);
+                        } else {
+                            if (t == 0) wait(&full[ek % NST], (unsigned)(ek / NST) & 1u);
+                            if (!ok) break;
+                            issue_s(t, ek);
+                            if (t == nt - 1) umma_commit(&empty[ek % NST]);
+                        }
+                    }
+                }
+                e += 2 * n;
+                for (int t = 0; t < nt; ++t) ++n_q[t];
+            } while (ok && w.next(a));
+            if (!ok) *s_fail = 1;
+            umma_commit(fin);
+            if (!mbar_wait(fin, 0)) *s_fail = 1;
+        }
+    } else if (busy && warp == 2) {
+        // ---- values of keys that no row sees become zero ----
+        int e = 1;
+        bool ok = true;
+        do {
+            const PtItem &x = w.x;
+            for (int i = w.i0; ok && i < w.i0 + w.n; ++i, e += 2) {
+                // the key tile first: copies may land out of order, and a stage's
+                // parity names its lap only once the lap before has landed
+                const int s = e % NST, sk = (e - 1) % NST;
+                ok = __all_sync(0xffffffffu, !*s_fail && mbar_wait(&full[sk], (unsigned)((e - 1) / NST) & 1u) &&
+                                                 mbar_wait(&full[s], (unsigned)(e / NST) & 1u));
+                if (!ok) break;
+                const int k0 = x.tile(i) * kPtKeys;
+                if (!(k0 + kPtKeys <= x.len && (k0 >= x.lo || k0 + kPtKeys <= x.sk))) {
+                    unsigned char *st = ring + s * kPtTile;
+                    for (int r = lane; r < kPtKeys; r += 32) {
+                        const int key = k0 + r;
+                        if (key < x.len && (key >= x.lo || key < x.sk)) continue;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            *reinterpret_cast<uint4 *>(st + (c >> 3) * kPtHalf + r * 128 + 16 * (c & 7)) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_ready[s]);
+            }
+        } while (ok && w.next(a));
+        if (!ok) *s_fail = 1;
+    } else if (busy && warp >= 4) {
+        // ---- softmax: thread = row of tile t ----
+        const int t = (warp - 4) >> 2, qd = warp & 3;
+        const int r = 32 * qd + lane;
+        const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
+        const uint32_t scol = tmem + lane_off + kPtS + 128u * t, ocol = tmem + lane_off + kPtO + 128u * t;
+        unsigned n_s = 0, seg = 0;  // phases
+        bool ok = true;
+        do {
+            const PtItem &x = w.x;
+            if (t == 1 && x.ntok <= a.tb) continue;  // (continue evaluates the loop's condition)
+            const int tok = t * a.tb + r / a.g;      // token of the item
+            const int head = w.j * a.g + r % a.g;
+            const bool live = r < a.tb * a.g && tok < x.ntok;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int64_t row = x.row0 + tok;
+            // the last key this row sees, and the first of its window
+            int p = x.p0 + tok;
+            if (a.shared > 0 && live) p = min(a.shared, paged_len(a.v, (int)row)) - 1;
+            const int lo = pt_window(a, p);
+            // the same of all rows of this warp: tiles up to the one and from the other need no mask
+            const int all_p = __reduce_min_sync(0xffffffffu, live ? p : 0x7fffffff);
+            const int all_lo = __reduce_max_sync(0xffffffffu, live ? lo : 0);
+
+            // q row into shared memory, 128-byte swizzle
+            {
+                unsigned char *dst = s_q + t * SM::QPARTS * kPtTile + r * 128;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {  // chunks of 8 values
+                    unsigned char *d = dst + (c >> 3) * kPtHalf + (((c & 7) ^ (r & 7)) << 4);
+                    if (QF32) {
+                        float4 f0 = make_float4(0.f, 0.f, 0.f, 0.f), f1 = f0;
+                        if (live) {
+                            const float4 *qp = reinterpret_cast<const float4 *>(
+                                static_cast<const float *>(a.q) + row * a.q_ts + head * a.q_hs + 8 * c);
+                            f0 = qp[0];
+                            f1 = qp[1];
+                        }
+                        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            h[y] = pack_bf16x2(f[2 * y], f[2 * y + 1]);
+                            l[y] = pack_bf16x2(f[2 * y] - bf16lo(h[y]), f[2 * y + 1] - bf16hi(h[y]));
+                        }
+                        *reinterpret_cast<uint4 *>(d) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4 *>(d + kPtTile) = make_uint4(l[0], l[1], l[2], l[3]);
+                    } else {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (live)
+                            u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + row * a.q_ts +
+                                                                 head * a.q_hs + 8 * c);
+                        *reinterpret_cast<uint4 *>(d) = u;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_ready[t]);
+            }
+            float m = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
+            for (int i = 0; i < w.n; ++i) {
+                ok = __all_sync(0xffffffffu, !*s_fail && mbar_wait(&s_full[t], n_s & 1u));
+                if (!ok) break;
+                ++n_s;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                if (warp_live) {
+                    float s[kPtKeys];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(scol + 32 * c, s + 32 * c);
+                    tmem_ld_wait();
+                    const int k0 = x.tile(w.i0 + i) * kPtKeys;
+                    const bool all = k0 + kPtKeys - 1 <= all_p && (k0 >= all_lo || k0 + kPtKeys <= a.sinks);
+                    if (!all) {
+#pragma unroll
+                        for (int e = 0; e < kPtKeys; ++e) {
+                            const int key = k0 + e;
+                            if (!(key <= p && (key >= lo || key < a.sinks))) s[e] = -INFINITY;
+                        }
+                    }
+                    float mx = s[0];
+#pragma unroll
+                    for (int e = 1; e < kPtKeys; ++e) mx = fmaxf(mx, s[e]);
+                    mx *= a.scale_log2;
+                    // raise the running maximum only when this tile exceeds it by > 8
+                    const bool need = mx > m + kAmLazy;
+                    if (__any_sync(0xffffffffu, need)) {
+                        const float mn = need ? mx : m;
+                        const float f = need ? exp2f(m - mn) : 1.f;  // 0 on the first step (m = -inf)
+                        if (i > 0) {
+                            // S of this tile was committed after the last P V of this row, so O is at rest
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                float v[32];
+                                tmem_ld32(ocol + 32 * c, v);
+                                tmem_ld_wait();
+                                uint32_t u[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
+                                tmem_st32(ocol + 32 * c, u);
+                            }
+                        }
+                        l *= f;
+                        m = mn;
+                    }
+                    const float sub = m == -INFINITY ? 0.f : m;  // no key seen yet: every term is 2^-inf
+                    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t u[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float p0 = ex2(fmaf(s[64 * c + 2 * e], a.scale_log2, -sub));
+                            const float p1 = ex2(fmaf(s[64 * c + 2 * e + 1], a.scale_log2, -sub));
+                            l0 += p0;
+                            l1 += p1;
+                            u[e] = pack_bf16x2(p0, p1);
+                        }
+                        tmem_st32(scol + 32 * c, u);
+                    }
+                    l += l0 + l1;
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, !*s_fail && mbar_wait(&o_full[t], seg & 1u));
+            if (!ok) break;
+            ++seg;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const bool done = a.shared == 0 && w.whole();
+            const float inv = 1.f / l;
+            const int64_t slot = a.shared > 0 ? (int64_t)w.idx + cta : 2 * cta + (w.first ? 0 : 1);
+            float *po = a.part_o + (slot * a.part_rows + 128 * t + r) * 128;
+            if (warp_live) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    tmem_ld32(ocol + 32 * c, v);
+                    tmem_ld_wait();
+                    if (live && done) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            u[e] = l != 0.f ? pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+                        uint4 *d = reinterpret_cast<uint4 *>(a.o + (row * a.nq + head) * 128 + 32 * c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<float4 *>(po + 32 * c)[e] =
+                                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    }
+                }
+                if (live && done) {
+                    if (a.lse) a.lse[row * a.nq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                } else if (live) {
+                    float *pm = a.part_ml + (slot * a.part_rows + 128 * t + r) * 2;
+                    pm[0] = m;
+                    pm[1] = l;
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty[t]);
+            // the first CTA of a cut item leaves its place for the join
+            if (t == 0 && r == 0 && a.cut && w.i0 == 0 && !done) {
+                const int last = am_cta_of(U, G, w.u + x.ntk - 1);
+                a.cut[cta] = make_int4(x.row0, x.ntok | (w.first ? 0 : 1 << 30), w.j, last - cta + 1);
+            }
+        } while (w.next(a));
+        if (!ok) *s_fail = 1;
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (*s_fail && threadIdx.x == 0) {
+        record_error(8u);
+        const int e1 = *s_issued;
+        for (int e = e1 > NST ? e1 - NST : 0; e < e1; ++e) mbar_wait(&full[e % NST], (unsigned)(e / NST) & 1u);
+    }
+    __syncthreads();
+    if (warp == 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// Joins the partials of the items that were cut: block (c, part) takes 32 rows
+// of the item whose first CTA is c; a warp per row, four dimensions per lane.
+constexpr int kPtJoinRows = 32;
+constexpr int kPtJoinThreads = 256;
+
+__device__ __forceinline__ void paged_store_row(const float4 &num, float M, float den, int lane, int64_t row,
+                                                __nv_bfloat16 *o, float *lse) {
+    const float inv = 1.f / den;
+    uint2 u = make_uint2(0u, 0u);
+    if (den != 0.f) u = make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+    reinterpret_cast<uint2 *>(o + row * 128)[lane] = u;
+    if (lse && lane == 0) lse[row] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+}
+
+__device__ __forceinline__ void paged_add_part(float4 &num, float &den, float M, float m, float l, const float4 *part) {
+    if (m == -INFINITY) return;  // nothing seen: the part's outputs may be anything
+    const float wt = exp2f(m - M);
+    const float4 x = __ldcg(part);
+    num.x += wt * x.x;
+    num.y += wt * x.y;
+    num.z += wt * x.z;
+    num.w += wt * x.w;
+    den += wt * l;
+}
+
+__global__ void __launch_bounds__(kPtJoinThreads) paged_prompt_join_kernel(const __grid_constant__ PagedPromptArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 cut = a.cut[c];
+    if (cut.w == 0) return;
+    const int ntok = cut.y & 0xffff, slot0 = 2 * c + (cut.y >> 30 & 1);
+    for (int k = warp; k < kPtJoinRows; k += kPtJoinThreads / 32) {
+        const int rr = blockIdx.y * kPtJoinRows + k, r = rr & 127;
+        const int tok = (rr >> 7) * a.tb + r / a.g;
+        if (r >= a.tb * a.g || tok >= ntok) continue;
+        const int64_t row = (int64_t)(cut.x + tok) * a.nq + cut.z * a.g + r % a.g;
+        auto part = [&](int x) { return (int64_t)(x == 0 ? slot0 : 2 * (c + x)) * a.part_rows + rr; };
+        float M = -INFINITY, den = 0.f;
+        for (int x = 0; x < cut.w; ++x) M = fmaxf(M, __ldcg(a.part_ml + part(x) * 2));
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < cut.w; ++x) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + part(x));
+            paged_add_part(num, den, M, ml.x, ml.y, reinterpret_cast<const float4 *>(a.part_o) + part(x) * 32 + lane);
+        }
+        paged_store_row(num, M, den, lane, row, a.o, a.lse);
+    }
+}
+
+// Joins, for every (sequence, query head) of a batch behind a common prefix,
+// the prefix's partials and what the sequence's own keys gave.
+struct PagedSharedJoinArgs {
+    PagedPromptArgs p;
+    int G;                       // CTAs the prefix was cut into
+    const float *own_o, *own_ml; // [n_seqs][nq][128], [n_seqs][nq][2]
+};
+
+__global__ void __launch_bounds__(kPtJoinThreads) paged_shared_join_kernel(const __grid_constant__ PagedSharedJoinArgs g) {
+    pdl_wait();
+    pdl_trigger();
+    const PagedPromptArgs &a = g.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * (kPtJoinThreads / 32) + warp;
+    if (row >= (int64_t)a.v.n_tokens * a.nq) return;
+    const int b = (int)(row / a.nq), head = (int)(row % a.nq), j = head / a.g;
+    const int items = pt_items(a, a.v.n_tokens), it = b / (2 * a.tb), tok = b % (2 * a.tb);
+    const int rr = tok / a.tb * 128 + tok % a.tb * a.g + head % a.g;
+    const int64_t NT = (a.shared + kPtKeys - 1) / kPtKeys, idx = (int64_t)j * items + it;
+    const int64_t U = NT * items * a.v.nkv;
+    const int cf = am_cta_of(U, g.G, idx * NT), cl = am_cta_of(U, g.G, idx * NT + NT - 1);
+    auto part = [&](int c) { return (idx + c) * a.part_rows + rr; };
+    const float2 own = __ldcg(reinterpret_cast<const float2 *>(g.own_ml) + row);
+    float M = own.x, den = 0.f;
+    for (int c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(a.part_ml + part(c) * 2));
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = cf; c <= cl; ++c) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + part(c));
+        paged_add_part(num, den, M, ml.x, ml.y, reinterpret_cast<const float4 *>(a.part_o) + part(c) * 32 + lane);
+    }
+    paged_add_part(num, den, M, own.x, own.y, reinterpret_cast<const float4 *>(g.own_o) + row * 32 + lane);
+    paged_store_row(num, M, den, lane, row, a.o, a.lse);
+}
+
+}  // namespace tpl

@@ -32,6 +32,7 @@ TPL_OPT_PREFILL_SPLIT = 4
 TPL_OPT_PREFILL_TAIL = 5
 TPL_SPLIT_QKV, TPL_SPLIT_O, TPL_SPLIT_GU = 1, 2, 4
 TPL_SPLIT_DEFAULT = TPL_SPLIT_QKV | TPL_SPLIT_O | TPL_SPLIT_GU
+TPL_BF16, TPL_F32 = 0, 1
 TPL_ATTN_STATIC_SCRATCH_BYTES = 4 * 1024 * 1024
 
 c_int32, c_int64, c_size_t, c_void_p, c_uint32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_uint32
@@ -64,6 +65,19 @@ class tpl_layer_weights(ctypes.Structure):
 
 class tpl_kv(ctypes.Structure):
     _fields_ = [("k", c_void_p), ("v", c_void_p), ("batch_cap", c_int32), ("seq_cap", c_int64)]
+
+
+class tpl_paged_kv(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("n_pages", c_int32), ("page_size", c_int32)]
+
+
+class tpl_paged_batch(ctypes.Structure):
+    _fields_ = [("page_table", c_void_p), ("table_stride", c_int64), ("max_pages", c_int32), ("n_seqs", c_int32),
+                ("kv_len", c_void_p), ("q_start", c_void_p), ("n_tokens", c_int32)]
+
+
+class tpl_heads(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("type", c_int32), ("token_stride", c_int64), ("head_stride", c_int64)]
 
 
 def _sig(name, restype, *argtypes):
@@ -118,6 +132,13 @@ _sig("tpl_reduce_partials", ctypes.c_int, _plan_p, c_void_p, c_void_p, c_int32, 
      c_void_p)
 _sig("tpl_mlp_block", ctypes.c_int, _plan_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_size_t,
      c_int32, c_void_p)
+_sig("tpl_paged_workspace_size", ctypes.c_int, _plan_p, c_int32, c_int32, P(c_size_t))
+_sig("tpl_paged_append", ctypes.c_int, _plan_p, P(tpl_paged_kv), P(tpl_paged_batch), P(tpl_heads), P(tpl_heads),
+     P(tpl_heads), P(tpl_heads), c_void_p)
+_sig("tpl_paged_attn", ctypes.c_int, _plan_p, P(tpl_paged_kv), P(tpl_paged_batch), P(tpl_heads), c_int32, c_int32,
+     c_void_p, c_void_p, c_void_p, c_size_t, c_void_p)
+_sig("tpl_paged_attn_shared", ctypes.c_int, _plan_p, P(tpl_paged_kv), P(tpl_paged_batch), c_int64, P(tpl_heads),
+     c_void_p, c_void_p, c_void_p, c_size_t, c_void_p)
 _sig("tpl_reduction_count", c_int64, _plan_p)
 _sig("tpl_decode_kernel_count", ctypes.c_int, _plan_p, c_int32, c_int32, c_int32, P(c_int32))
 _sig("tpl_reset_counters", None, _plan_p)
@@ -205,6 +226,39 @@ def _ptr(t):
 def _stream():
     import torch
     return torch.cuda.current_stream().cuda_stream
+
+
+def _on_current_device(*tensors) -> None:
+    """The library takes plain pointers, so a tensor that is elsewhere is
+    refused here (None: an argument left out)."""
+    import torch
+    for x in tensors:
+        if x is None:
+            continue
+        if not x.is_cuda:
+            raise ValueError("a paged-cache tensor is not on a CUDA device")
+        if x.device.index != torch.cuda.current_device():
+            raise ValueError(f"a paged-cache tensor is on {x.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+
+
+class PagedKV:
+    """tpl_paged_kv over two pool tensors, which it keeps alive."""
+
+    def __init__(self, k, v):
+        self.k, self.v = k, v
+        self.c = tpl_paged_kv(k.data_ptr(), v.data_ptr(), k.shape[1], k.shape[3])
+
+
+class PagedBatch:
+    """tpl_paged_batch over device arrays, which it keeps alive."""
+
+    def __init__(self, page_table, kv_len, q_start, n_tokens):
+        self.page_table, self.kv_len, self.q_start, self.n_tokens = page_table, kv_len, q_start, n_tokens
+        n, entries = page_table.shape
+        stride = page_table.stride(0) if n > 1 else max(entries, page_table.stride(0))
+        self.c = tpl_paged_batch(page_table.data_ptr(), stride, entries, n, kv_len.data_ptr(), _ptr(q_start),
+                                 n_tokens)
 
 
 class Plan:
@@ -378,6 +432,119 @@ class Plan:
     def mlp_block(self, packed, x, y=None, y32=None, ws=None, mode=TPL_REDUCE_FUSED):
         check(tpl_mlp_block(self.handle, packed.data_ptr(), x.data_ptr(), x.shape[0], _ptr(y), _ptr(y32),
                             ws.data_ptr(), ws.numel(), mode, _stream()), "tpl_mlp_block")
+
+    # ---- the paged cache ----
+    def paged_kv(self, k, v) -> PagedKV:
+        """The pool: contiguous bf16 tensors [t][n_pages][n_kv/t][page_size][d]."""
+        import torch
+        d = self.dims
+        for x in (k, v):
+            if x.dtype != torch.bfloat16 or x.dim() != 5 or not x.is_contiguous():
+                raise ValueError("paged_kv: the pool is a contiguous bf16 tensor [t][n_pages][n_kv/t][page_size][d]")
+            if (x.shape[0], x.shape[2], x.shape[4]) != (self.t, d.n_kv_heads // self.t, d.head_dim):
+                raise ValueError(f"paged_kv: pool {tuple(x.shape)} does not fit t={self.t}, n_kv={d.n_kv_heads}, "
+                                 f"head_dim={d.head_dim}")
+        if k.shape != v.shape:
+            raise ValueError("paged_kv: k and v differ in shape")
+        _on_current_device(k, v)
+        return PagedKV(k, v)
+
+    @staticmethod
+    def paged_batch(page_table, kv_len, q_start=None, n_tokens=None) -> PagedBatch:
+        """page_table [n_seqs][max_pages], kv_len [n_seqs] and q_start
+        [n_seqs + 1] (None: one token per sequence), int32 on the device;
+        n_tokens: rows of q (needed with q_start: its contents are not read here)."""
+        import torch
+        for x in (page_table, kv_len, q_start):
+            if x is not None and (x.dtype != torch.int32 or (x.numel() > 1 and x.stride(-1) != 1)):
+                raise ValueError("paged_batch: the arrays are int32, contiguous along their last dimension")
+        if page_table.dim() != 2 or kv_len.shape != page_table.shape[:1]:
+            raise ValueError("paged_batch: page_table is [n_seqs][max_pages], kv_len [n_seqs]")
+        n = page_table.shape[0]
+        if q_start is None:
+            if n_tokens not in (None, n):
+                raise ValueError("paged_batch: without q_start there is one token per sequence")
+            n_tokens = n
+        elif q_start.shape != (n + 1,) or n_tokens is None:
+            raise ValueError("paged_batch: q_start is [n_seqs + 1] and needs n_tokens")
+        _on_current_device(page_table, kv_len, q_start)
+        return PagedBatch(page_table, kv_len, q_start, n_tokens)
+
+    def paged_workspace_size(self, n_seqs: int, n_tokens: int) -> int:
+        out = c_size_t()
+        check(tpl_paged_workspace_size(self.handle, n_seqs, n_tokens, ctypes.byref(out)), "tpl_paged_workspace_size")
+        return out.value
+
+    def paged_workspace(self, n_seqs: int, n_tokens: int, device="cuda"):
+        import torch
+        n = self.paged_workspace_size(n_seqs, n_tokens)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        check(tpl_workspace_init(self.handle, ws.data_ptr(), n, _stream()), "tpl_workspace_init")
+        return ws
+
+    @staticmethod
+    def _heads(x, rows: int, heads: int, head_dim: int, name: str):
+        """tpl_heads of a tensor [rows][heads][head_dim] with any strides
+        between its heads (or [rows][heads * head_dim])."""
+        import torch
+        if x is None:
+            return None
+        if x.dim() == 2 and x.shape[1] == heads * head_dim:
+            x = x.unflatten(1, (heads, head_dim))
+        if tuple(x.shape) != (rows, heads, head_dim) or (rows > 0 and x.stride(2) != 1):
+            raise ValueError(f"{name}: expected [{rows}][{heads}][{head_dim}] with contiguous heads, got "
+                             f"{tuple(x.shape)}")
+        if x.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"{name}: bf16 or fp32, got {x.dtype}")
+        _on_current_device(x)
+        ts, hs, _ = x.stride()
+        # a dimension of one element has no stride of its own
+        ts, hs = (ts if rows > 1 else heads * head_dim), (hs if heads > 1 else head_dim)
+        return ctypes.byref(tpl_heads(x.data_ptr(), TPL_F32 if x.dtype == torch.float32 else TPL_BF16, ts, hs))
+
+    def _paged_out(self, batch, o, lse, name):
+        import torch
+        d, n = self.dims, batch.n_tokens
+        if o.dtype != self.act_dtype or o.numel() != n * d.n_q_heads * d.head_dim or not o.is_contiguous():
+            raise ValueError(f"{name}: o is a contiguous {self.act_dtype} tensor [{n}][{d.n_q_heads * d.head_dim}]")
+        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, d.n_q_heads) or
+                                not lse.is_contiguous()):
+            raise ValueError(f"{name}: lse is a contiguous fp32 tensor [{n}][{d.n_q_heads}]")
+        _on_current_device(o, lse)
+
+    def paged_append(self, kv: PagedKV, batch: PagedBatch, k, v, q=None, q_out=None):
+        """Put k, v [n_tokens][n_kv][d] into their slots (turned with TPL_ROPE)
+        and q [n_tokens][n_q][d], turned, into q_out (default: in place)."""
+        d, n = self.dims, batch.n_tokens
+        if q_out is None:
+            q_out = q
+        _on_current_device(kv.k, kv.v, batch.page_table, batch.kv_len, batch.q_start)
+        check(tpl_paged_append(self.handle, ctypes.byref(kv.c), ctypes.byref(batch.c),
+                               self._heads(q, n, d.n_q_heads, d.head_dim, "paged_append: q"),
+                               self._heads(q_out, n, d.n_q_heads, d.head_dim, "paged_append: q_out"),
+                               self._heads(k, n, d.n_kv_heads, d.head_dim, "paged_append: k"),
+                               self._heads(v, n, d.n_kv_heads, d.head_dim, "paged_append: v"), _stream()),
+              "tpl_paged_append")
+
+    def paged_attn(self, kv: PagedKV, batch: PagedBatch, q, o, ws, window: int = 0, sinks: int = 0, lse=None):
+        """Attention of the batch's tokens over their pages into o (and lse)."""
+        d = self.dims
+        self._paged_out(batch, o, lse, "paged_attn")
+        _on_current_device(kv.k, kv.v, batch.page_table, batch.kv_len, batch.q_start, ws)
+        check(tpl_paged_attn(self.handle, ctypes.byref(kv.c), ctypes.byref(batch.c),
+                             self._heads(q, batch.n_tokens, d.n_q_heads, d.head_dim, "paged_attn: q"), window, sinks,
+                             o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream()), "tpl_paged_attn")
+
+    def paged_attn_shared(self, kv: PagedKV, batch: PagedBatch, shared_len: int, q, o, ws, lse=None):
+        """paged_attn of a decode batch whose sequences all begin with the same
+        shared_len keys (the same first pages), which are read once."""
+        d = self.dims
+        self._paged_out(batch, o, lse, "paged_attn_shared")
+        _on_current_device(kv.k, kv.v, batch.page_table, batch.kv_len, batch.q_start, ws)
+        check(tpl_paged_attn_shared(self.handle, ctypes.byref(kv.c), ctypes.byref(batch.c), shared_len,
+                                    self._heads(q, batch.n_tokens, d.n_q_heads, d.head_dim, "paged_attn_shared: q"),
+                                    o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream()),
+              "tpl_paged_attn_shared")
 
     def last_device_error(self) -> int:
         return tpl_last_device_error(self.handle, _stream())
