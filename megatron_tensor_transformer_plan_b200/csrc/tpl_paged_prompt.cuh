@@ -22,7 +22,7 @@
 //   3     idle;
 //   4-7   softmax of tile 0, 8-11 softmax of tile 1: one thread per row.
 // S = Q K^T reads Q (bf16, or bf16 hi + lo when q is fp32: two products) and K
-// from shared memory; P replaces S in tensor memory as bf16; O += P V.  The
+// from shared memory; P replaces half of S in tensor memory as bf16; O += P V.  The
 // two tiles alternate, so the MMAs of one run under the softmax of the other.
 // P has one bf16 part: with o rounded to bf16 anyway, the two roundings are of
 // the same size (2^-9 of each term against 2^-9 of the sum); the denominator
@@ -185,7 +185,40 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Two fp32 values at a time: the fma and add units take packed pairs.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Uses of a loaded row stay behind the wait for it.
+__device__ __forceinline__ void tmem_ld_done(float *v) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                          "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -376,14 +409,30 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         bool ok = true;
         do {
             const PtItem &x = w.x;
+            const int seq = a.shared > 0 ? 0 : w.b;
+            const int64_t jrow = (int64_t)(w.j / a.v.nkv_s) * a.v.n_pages * a.v.nkv_s + w.j % a.v.nkv_s;
+            // the page of this lane's part of tile i; the next tile's entry is fetched
+            // before this one's stages are waited for
+            auto entry = [&](int i, int &key, bool &want) {
+                key = x.tile(i) * kPtKeys + (sub << box_shift);
+                want = half < 2 && key < x.len && (key + (1 << box_shift) > x.lo || key < x.sk);
+                return want ? a.v.table[seq * a.v.table_stride + (key >> a.v.page_shift)] : 0;
+            };
+            int key_n;
+            bool want_n;
+            int page_n = entry(w.i0, key_n, want_n);
             for (int i = w.i0; ok && i < w.i0 + w.n; ++i) {
-                const int key = x.tile(i) * kPtKeys + (sub << box_shift);
-                const bool want = half < 2 && key < x.len && (key + (1 << box_shift) > x.lo || key < x.sk);
-                int row = 0;
-                if (want) {
-                    const int64_t r = paged_row(a.v, a.shared > 0 ? 0 : w.b, key >> a.v.page_shift, w.j);
-                    row = r < 0 ? 0 : (int)r + (key & ((1 << a.v.page_shift) - 1));
+                const int key = key_n;
+                const bool want = want_n;
+                int page = page_n;
+                if (i + 1 < w.i0 + w.n) page_n = entry(i + 1, key_n, want_n);
+                if (want && (page < 0 || page >= a.v.n_pages)) {
+                    record_error(kErrPaged);
+                    page = 0;
                 }
+                const int row = want ? (int)((jrow + (int64_t)page * a.v.nkv_s) << a.v.page_shift) +
+                                           (key & ((1 << a.v.page_shift) - 1))
+                                     : 0;
                 const unsigned bytes = (unsigned)__popc(__ballot_sync(0xffffffffu, want)) << (box_shift + 7);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++e) {
@@ -432,7 +481,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             auto issue_pv = [&](int t, int ev, bool acc) {  // O_t += P_t V
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const unsigned vb = smem_u32(ring + (ev % NST) * kPtTile);
-                const uint32_t pcol = tmem + kPtS + 128u * t;
+                const uint32_t pcol = tmem + kPtS + 128u * t + 64u;  // P lies in the second half of S
 #pragma unroll
                 for (int ks = 0; ks < kPtKeys / 16; ++ks)
                     umma_ts(tmem + kPtO + 128u * t, pcol + 8 * ks, umma_desc_lbo(vb + 2048 * ks, kPtHalf), IDESC_PV,
@@ -571,23 +620,32 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                 ++n_s;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 if (warp_live) {
-                    float s[kPtKeys];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(scol + 32 * c, s + 32 * c);
-                    tmem_ld_wait();
                     const int k0 = x.tile(w.i0 + i) * kPtKeys;
                     const bool all = k0 + kPtKeys - 1 <= all_p && (k0 >= all_lo || k0 + kPtKeys <= a.sinks);
-                    if (!all) {
+                    auto mask = [&](float *s, int key0) {  // 32 logits from key key0
+                        if (all) return;
 #pragma unroll
-                        for (int e = 0; e < kPtKeys; ++e) {
-                            const int key = k0 + e;
-                            if (!(key <= p && (key >= lo || key < a.sinks))) s[e] = -INFINITY;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(key0 + e <= p && (key0 + e >= lo || key0 + e < a.sinks))) s[e] = -INFINITY;
+                    };
+                    // the maximum first; the row's second half stays in registers, the first
+                    // is loaded again for its exponentials
+                    float s[64], mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_ld32(scol + 64 * h, s);
+                        tmem_ld32(scol + 64 * h + 32, s + 32);
+                        tmem_ld_wait();
+                        tmem_ld_done(s);
+                        tmem_ld_done(s + 32);
+                        mask(s, k0 + 64 * h);
+                        mask(s + 32, k0 + 64 * h + 32);
+#pragma unroll
+                        for (int e = 0; e < 64; e += 8)  // four chains: one would be latency
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) mc[c] = max3(mc[c], s[e + c], s[e + 4 + c]);
                     }
-                    float mx = s[0];
-#pragma unroll
-                    for (int e = 1; e < kPtKeys; ++e) mx = fmaxf(mx, s[e]);
-                    mx *= a.scale_log2;
+                    const float mx = max3(fmaxf(mc[0], mc[1]), mc[2], mc[3]) * a.scale_log2;
                     // raise the running maximum only when this tile exceeds it by > 8
                     const bool need = mx > m + kAmLazy;
                     if (__any_sync(0xffffffffu, need)) {
@@ -600,6 +658,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                                 float v[32];
                                 tmem_ld32(ocol + 32 * c, v);
                                 tmem_ld_wait();
+                                tmem_ld_done(v);
                                 uint32_t u[32];
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
@@ -610,20 +669,37 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                         m = mn;
                     }
                     const float sub = m == -INFINITY ? 0.f : m;  // no key seen yet: every term is 2^-inf
-                    float l0 = 0.f, l1 = 0.f;
+                    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), sub2 = pack2(-sub, -sub);
+                    uint64_t l2[2] = {0, 0};
+                    // P (bf16) replaces the row's second half: keys 0-63, then 64-127
+                    auto exps = [&](const float *v, int chunk) {
+                        uint32_t u[16];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t u[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float p0 = ex2(fmaf(s[64 * c + 2 * e], a.scale_log2, -sub));
-                            const float p1 = ex2(fmaf(s[64 * c + 2 * e + 1], a.scale_log2, -sub));
-                            l0 += p0;
-                            l1 += p1;
+                        for (int e = 0; e < 16; ++e) {
+                            float x0, x1;
+                            unpack2(fma2(pack2(v[2 * e], v[2 * e + 1]), scale2, sub2), x0, x1);
+                            const float p0 = ex2(x0), p1 = ex2(x1);
+                            l2[e & 1] = add2(l2[e & 1], pack2(p0, p1));
                             u[e] = pack_bf16x2(p0, p1);
                         }
-                        tmem_st32(scol + 32 * c, u);
-                    }
+                        tmem_st16(scol + 64 + 16 * chunk, u);
+                    };
+                    float r0[32];
+                    tmem_ld32(scol, r0);
+                    exps(s, 2);
+                    exps(s + 32, 3);
+                    tmem_ld_wait();
+                    tmem_ld_done(r0);
+                    mask(r0, k0);
+                    float r1[32];
+                    tmem_ld32(scol + 32, r1);
+                    exps(r0, 0);
+                    tmem_ld_wait();
+                    tmem_ld_done(r1);
+                    mask(r1, k0 + 32);
+                    exps(r1, 1);
+                    float l0, l1;
+                    unpack2(add2(l2[0], l2[1]), l0, l1);
                     l += l0 + l1;
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
@@ -646,6 +722,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                     float v[32];
                     tmem_ld32(ocol + 32 * c, v);
                     tmem_ld_wait();
+                    tmem_ld_done(v);
                     if (live && done) {
                         uint32_t u[16];
 #pragma unroll
