@@ -13,14 +13,15 @@
 // unnormalised output) per CTA in the workspace; a second kernel joins them.
 // Neighbouring CTAs work on the same kv head, so its keys come from L2.
 //
-// 12 warps:
-//   0     TMA producer: K and V tiles in turn into a ring, a lane per page
-//         part (64 dims of at most 128 keys of one page), no multicast;
+// 20 warps:
+//   0, 3  TMA producers of the K and of the V tiles, in turn into a ring, a lane
+//         per page part (64 dims of at most 128 keys of one page), no multicast;
 //   1     TMEM owner and MMA issuer (one thread);
 //   2     replaces the values of keys that no row sees by zero (0 * NaN is NaN)
 //         in the tiles that have such keys, before the MMA reads them;
-//   3     idle;
-//   4-7   softmax of tile 0, 8-11 softmax of tile 1: one thread per row.
+//   4-11  softmax of tile 0, 12-19 softmax of tile 1: two threads per row, 64 of
+//         a tile's 128 keys each.  They share the row's maximum through shared
+//         memory; four warps per scheduler hide one another's latencies.
 // S = Q K^T reads Q (bf16, or bf16 hi + lo when q is fp32: two products) and K
 // from shared memory; P replaces half of S in tensor memory as bf16; O += P V.  The
 // two tiles alternate, so the MMAs of one run under the softmax of the other.
@@ -54,8 +55,8 @@ struct PtSmem {
     static constexpr int QPARTS = QF32 ? 2 : 1;
     static constexpr int NST = QF32 ? 3 : 5;   // ring stages of one tile; odd: see v_ready
     static constexpr int Q = 2 * QPARTS * kPtTile;
-    static constexpr int BAR = 1536;
-    static constexpr size_t BYTES = (size_t)Q + NST * kPtTile + BAR + 1024;
+    static constexpr int BAR = 3072;
+    static constexpr size_t BYTES = (size_t)Q + NST * kPtTile + BAR;
     static_assert(BYTES <= 232448, "shared memory per block");
     static_assert(NST % 2 == 1, "K and V alternate on every stage");
 };
@@ -212,6 +213,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// The n lowest bits (none for n <= 0, all from n = 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 // Uses of a loaded row stay behind the wait for it.
 __device__ __forceinline__ void tmem_ld_done(float *v) {
 #pragma unroll
@@ -220,23 +224,16 @@ __device__ __forceinline__ void tmem_ld_done(float *v) {
                           "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
 template <bool QF32>
 __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __grid_constant__ PagedPromptArgs a) {
     using SM = PtSmem<QF32>;
     constexpr int NST = SM::NST;
     extern __shared__ __align__(1024) unsigned char pt_raw[];
-    unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)pt_raw + 1023) & ~(uintptr_t)1023);
+    unsigned char *sm = pt_raw;
+    if (smem_u32(sm) & 1023u) {  // (the whole grid: the swizzled tiles need 1 KB alignment)
+        if (threadIdx.x == 0) record_error(8u);
+        return;
+    }
     unsigned char *s_q = sm;              // [tile][part][half][128 rows][128 B]
     unsigned char *ring = sm + SM::Q;
     uint64_t *full = reinterpret_cast<uint64_t *>(ring + NST * kPtTile);  // [NST] tile landed
@@ -251,9 +248,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
     volatile int *s_fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_issued = const_cast<int *>(s_fail) + 1;
-    int *s_where = s_issued + 1;          // [4] start of this CTA's range: j, b, item, tiles before
+    int *s_where = s_issued + 2;          // [4] start of this CTA's range: j, b, item, tiles before
     long long *s_sum = reinterpret_cast<long long *>((reinterpret_cast<uintptr_t>(s_where + 4) + 7) & ~(uintptr_t)7);
-    static_assert((3 * NST + 11) * 8 + 32 + 16 + 16 * 8 <= SM::BAR, "barrier area");
+    float *s_x = reinterpret_cast<float *>(s_sum + kPtThreads / 32);  // [tile][half][128 rows]: a row's halves meet here
+    static_assert((3 * NST + 11) * 8 + 40 + 16 + kPtThreads / 32 * 8 + 2 * 2 * 128 * 4 <= SM::BAR, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
@@ -272,7 +270,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         }
         mbar_init(fin, 1);
         *s_fail = 0;
-        *s_issued = 0;
+        s_issued[0] = s_issued[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -400,51 +398,50 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         w.open(a);
     }
 
-    if (busy && warp == 0) {
-        // ---- TMA producer: lane = (dims half, page part) ----
+    if (busy && (warp == 0 || warp == 3)) {
+        // ---- TMA producers: warp 0 the keys (even ring elements), warp 3 the values.
+        //      The pages of 32 parts (whole tiles) are looked up at once, a batch ahead. ----
+        const int kv = warp == 0 ? 0 : 1;
         const int box_shift = min(a.v.page_shift, 7);
-        const int nsub = kPtKeys >> box_shift;  // at most 8
-        const int half = lane / nsub, sub = lane % nsub;
-        int e = 0;  // ring element: K and V of each tile in turn
+        const int nsub = kPtKeys >> box_shift;  // parts of a tile: at most 8
+        const int half = lane / nsub, sub = lane % nsub;  // this lane's copy (half < 2)
+        const int batch = 32 / nsub;            // tiles per lookup
+        int e = kv;
         bool ok = true;
         do {
             const PtItem &x = w.x;
-            const int seq = a.shared > 0 ? 0 : w.b;
+            const int seq = a.shared > 0 ? 0 : w.b, i1 = w.i0 + w.n;
             const int64_t jrow = (int64_t)(w.j / a.v.nkv_s) * a.v.n_pages * a.v.nkv_s + w.j % a.v.nkv_s;
-            // the page of this lane's part of tile i; the next tile's entry is fetched
-            // before this one's stages are waited for
-            auto entry = [&](int i, int &key, bool &want) {
-                key = x.tile(i) * kPtKeys + (sub << box_shift);
-                want = half < 2 && key < x.len && (key + (1 << box_shift) > x.lo || key < x.sk);
-                return want ? a.v.table[seq * a.v.table_stride + (key >> a.v.page_shift)] : 0;
+            // the page of part lane % nsub of tile i0 + lane / nsub: -1 when no key of it is seen
+            auto lookup = [&](int i0) {
+                const int i = i0 + lane / nsub, key = x.tile(min(i, i1 - 1)) * kPtKeys + ((lane % nsub) << box_shift);
+                const bool want = i < i1 && key < x.len && (key + (1 << box_shift) > x.lo || key < x.sk);
+                int page = -1;
+                if (want) page = max(a.v.table[seq * a.v.table_stride + (key >> a.v.page_shift)], -2);
+                return want && page < 0 ? -2 : page;
             };
-            int key_n;
-            bool want_n;
-            int page_n = entry(w.i0, key_n, want_n);
-            for (int i = w.i0; ok && i < w.i0 + w.n; ++i) {
-                const int key = key_n;
-                const bool want = want_n;
-                int page = page_n;
-                if (i + 1 < w.i0 + w.n) page_n = entry(i + 1, key_n, want_n);
-                if (want && (page < 0 || page >= a.v.n_pages)) {
+            int ahead = lookup(w.i0);
+            for (int ib = w.i0; ok && ib < i1; ib += batch) {
+                int page = ahead;
+                if (ib + batch < i1) ahead = lookup(ib + batch);
+                if (page == -2 || page >= a.v.n_pages) {
                     record_error(kErrPaged);
                     page = 0;
                 }
-                const int row = want ? (int)((jrow + (int64_t)page * a.v.nkv_s) << a.v.page_shift) +
-                                           (key & ((1 << a.v.page_shift) - 1))
-                                     : 0;
-                const unsigned bytes = (unsigned)__popc(__ballot_sync(0xffffffffu, want)) << (box_shift + 7);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++e) {
+                const int base = page < 0 ? -1 : (int)((jrow + (int64_t)page * a.v.nkv_s) << a.v.page_shift);
+                for (int i = ib; ok && i < min(ib + batch, i1); ++i, e += 2) {
+                    int row = __shfl_sync(0xffffffffu, base, (i - ib) * nsub + sub);
+                    const bool want = half < 2 && row >= 0;
+                    row += (x.tile(i) * kPtKeys + (sub << box_shift)) & ((1 << a.v.page_shift) - 1);
+                    const unsigned bytes = (unsigned)__popc(__ballot_sync(0xffffffffu, want)) << (box_shift + 7);
                     const int s = e % NST;
                     bool go = true;
-                    if (lane == 0) go = !*s_fail && mbar_wait(&empty[s], ((unsigned)(e / NST) & 1u) ^ 1u);
-                    if (!__all_sync(0xffffffffu, go)) {
-                        ok = false;
-                        break;
+                    if (lane == 0) {
+                        go = !*s_fail && mbar_wait(&empty[s], ((unsigned)(e / NST) & 1u) ^ 1u);
+                        if (go) mbar_expect_tx(&full[s], bytes);
                     }
-                    if (lane == 0) mbar_expect_tx(&full[s], bytes);
-                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, go);
+                    if (!ok) break;
                     if (want)
                         tma_load_2d(ring + s * kPtTile + half * kPtHalf + (sub << (box_shift + 7)),
                                     kv ? &a.tm_v : &a.tm_k, 64 * half, row, &full[s]);
@@ -452,7 +449,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             }
         } while (ok && w.next(a));
         if (!ok) *s_fail = 1;
-        if (lane == 0) *s_issued = e;
+        if (lane == 0) s_issued[kv] = e;
     } else if (busy && warp == 1) {
         if (lane == 0) {
             constexpr uint32_t IDESC_S = umma_idesc(128, kPtKeys);
@@ -624,9 +621,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                     const bool all = k0 + kPtKeys - 1 <= all_p && (k0 >= all_lo || k0 + kPtKeys <= a.sinks);
                     auto mask = [&](float *s, int key0) {  // 32 logits from key key0
                         if (all) return;
+                        // key <= p && (key >= lo || key < sinks), a bit per key
+                        const uint32_t vis = low_bits(p - key0 + 1) & (~low_bits(lo - key0) | low_bits(a.sinks - key0));
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!(key0 + e <= p && (key0 + e >= lo || key0 + e < a.sinks))) s[e] = -INFINITY;
+                            if (!(vis >> e & 1u)) s[e] = -INFINITY;
                     };
                     // the maximum first; the row's second half stays in registers, the first
                     // is loaded again for its exponentials
@@ -653,16 +652,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                         const float f = need ? exp2f(m - mn) : 1.f;  // 0 on the first step (m = -inf)
                         if (i > 0) {
                             // S of this tile was committed after the last P V of this row, so O is at rest
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                float v[16];
+                                tmem_ld16(ocol + 16 * c, v);
+                                uint32_t u[16];
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float v[32];
-                                tmem_ld32(ocol + 32 * c, v);
-                                tmem_ld_wait();
-                                tmem_ld_done(v);
-                                uint32_t u[32];
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
-                                tmem_st32(ocol + 32 * c, u);
+                                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * f);
+                                tmem_st16(ocol + 16 * c, u);
                             }
                         }
                         l *= f;
@@ -717,7 +714,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             const int64_t slot = a.shared > 0 ? (int64_t)w.idx + cta : 2 * cta + (w.first ? 0 : 1);
             float *po = a.part_o + (slot * a.part_rows + 128 * t + r) * 128;
             if (warp_live) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float v[32];
                     tmem_ld32(ocol + 32 * c, v);
@@ -761,8 +758,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     __syncthreads();
     if (*s_fail && threadIdx.x == 0) {
         record_error(8u);
-        const int e1 = *s_issued;
-        for (int e = e1 > NST ? e1 - NST : 0; e < e1; ++e) mbar_wait(&full[e % NST], (unsigned)(e / NST) & 1u);
+        for (int kv = 0; kv < 2; ++kv)  // the copies in flight: the last of the ring's laps
+            for (int e = s_issued[kv] - 2; e >= 0 && e >= s_issued[kv] - 2 * NST; e -= 2)
+                mbar_wait(&full[e % NST], (unsigned)(e / NST) & 1u);
     }
     __syncthreads();
     if (warp == 1) {
