@@ -55,7 +55,7 @@ struct PtSmem {
     static constexpr int QPARTS = QF32 ? 2 : 1;
     static constexpr int NST = QF32 ? 3 : 5;   // ring stages of one tile; odd: see v_ready
     static constexpr int Q = 2 * QPARTS * kPtTile;
-    static constexpr int BAR = 3072;
+    static constexpr int BAR = 1024;
     static constexpr size_t BYTES = (size_t)Q + NST * kPtTile + BAR;
     static_assert(BYTES <= 232448, "shared memory per block");
     static_assert(NST % 2 == 1, "K and V alternate on every stage");
@@ -213,6 +213,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// True in one lane of the warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred P; elect.sync _|P, 0xffffffff; selp.u32 %0, 1, 0, P; }" : "=r"(p));
+    return p != 0;
+}
+
 // The n lowest bits (none for n <= 0, all from n = 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
@@ -240,9 +247,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     uint64_t *empty = full + NST;         // [NST] tile read by its last MMA
     uint64_t *v_ready = empty + NST;      // [NST] V tile checked
     uint64_t *q_ready = v_ready + NST;    // [2]
-    uint64_t *s_full = q_ready + 2;       // [2]
-    uint64_t *p_full = s_full + 2;        // [2]
-    uint64_t *o_full = p_full + 2;        // [2]
+    uint64_t *s_full = q_ready + 2;       // [2 tiles][2 halves]
+    uint64_t *p_full = s_full + 4;        // [2][2]
+    uint64_t *pv_done = p_full + 4;       // [2]
+    uint64_t *o_full = pv_done + 2;       // [2]
     uint64_t *o_empty = o_full + 2;       // [2]
     uint64_t *fin = o_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
@@ -250,10 +258,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     int *s_issued = const_cast<int *>(s_fail) + 1;
     int *s_where = s_issued + 2;          // [4] start of this CTA's range: j, b, item, tiles before
     long long *s_sum = reinterpret_cast<long long *>((reinterpret_cast<uintptr_t>(s_where + 4) + 7) & ~(uintptr_t)7);
-    float *s_x = reinterpret_cast<float *>(s_sum + kPtThreads / 32);  // [tile][half][128 rows]: a row's halves meet here
-    static_assert((3 * NST + 11) * 8 + 40 + 16 + kPtThreads / 32 * 8 + 2 * 2 * 128 * 4 <= SM::BAR, "barrier area");
+    static_assert((3 * NST + 17) * 8 + 40 + 16 + kPtThreads / 32 * 8 <= SM::BAR, "barrier area");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
@@ -263,8 +270,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_ready[t], 4);
-            mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&s_full[2 * t + h], 1);
+                mbar_init(&p_full[2 * t + h], 4);
+            }
+            mbar_init(&pv_done[t], 1);
             mbar_init(&o_full[t], 1);
             mbar_init(&o_empty[t], 4);
         }
@@ -451,75 +461,100 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         if (!ok) *s_fail = 1;
         if (lane == 0) s_issued[kv] = e;
     } else if (busy && warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t IDESC_S = umma_idesc(128, kPtKeys);
-            constexpr uint32_t IDESC_PV = umma_idesc(128, 128) | (1u << 16);  // B (V) MN-major
-            int e = 0;                         // ring element of the segment's first K
-            unsigned n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of p_full, and of q_ready / o_empty
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, unsigned parity) {
-                if (ok && (*s_fail || !mbar_wait(bar, parity))) ok = false;
-                return ok;
-            };
-            auto issue_s = [&](int t, int ek) {  // S_t = Q_t K^T
+        // The whole warp walks, one elected lane issues: what the products take
+        // (addresses, descriptors) is then warp-uniform and stays in uniform
+        // registers.  Issued from a branch of one lane, every product waited
+        // about 100 cycles for its operands to be moved there.
+        constexpr uint32_t IDESC_S = umma_idesc(128, kPtKeys / 2);
+        constexpr uint32_t IDESC_PV = umma_idesc(128, 128) | (1u << 16);  // B (V) MN-major
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = umma_desc(smem_u32(s_q)), dk0 = umma_desc(smem_u32(ring)),
+                       dv0 = umma_desc_lbo(smem_u32(ring), kPtHalf);
+        constexpr unsigned TILE16 = kPtTile >> 4, HALF16 = kPtHalf >> 4, ROWS16 = 64 * 128 >> 4;  // (descriptors count 16 bytes)
+        int sk = 0, sv = 1;                // ring stages of the next K and V
+        unsigned lk = 0, lv = 0;           // and their laps (v_ready has a phase per two laps)
+        unsigned n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of p_full, and of q_ready / o_empty
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, unsigned parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
+        auto commit = [&](uint64_t *bar) {
+            if (elect_one()) umma_commit(bar);
+        };
+        auto issue_s = [&](int t, int h) {  // 64 keys of S_t = Q_t K^T
+            const uint64_t dk = dk0 + sk * TILE16 + h * ROWS16, da = dq + t * SM::QPARTS * TILE16;
+            const uint32_t d = tm + kPtS + 128u * t + 64u * h;
+            if (elect_one()) {
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned kb = smem_u32(ring + (ek % NST) * kPtTile);
-                const unsigned qb = smem_u32(s_q + t * SM::QPARTS * kPtTile);
-                const uint32_t d = tmem + kPtS + 128u * t;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
-                    const unsigned off = (unsigned)((kk >> 2) * kPtHalf + 32 * (kk & 3));
-                    const uint64_t dk = umma_desc(kb + off);
-                    umma(d, umma_desc(qb + off), dk, IDESC_S, kk > 0 ? 1u : 0u);
-                    if (QF32) umma(d, umma_desc(qb + kPtTile + off), dk, IDESC_S, 1u);
+                    const unsigned off = (kk >> 2) * HALF16 + 2 * (kk & 3);
+                    umma(d, da + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
+                    if (QF32) umma(d, da + TILE16 + off, dk + off, IDESC_S, 1u);
                 }
-                umma_commit(&s_full[t]);
-            };
-            auto issue_pv = [&](int t, int ev, bool acc) {  // O_t += P_t V
+                umma_commit(&s_full[2 * t + h]);
+            }
+        };
+        auto issue_pv = [&](int t, int h, bool acc) {  // O_t += P_t V over 64 keys
+            const uint64_t dv = dv0 + sv * TILE16 + h * ROWS16;
+            const uint32_t pcol = tm + kPtS + 128u * t + 64u * h, d = tm + kPtO + 128u * t;
+            if (elect_one()) {
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned vb = smem_u32(ring + (ev % NST) * kPtTile);
-                const uint32_t pcol = tmem + kPtS + 128u * t + 64u;  // P lies in the second half of S
 #pragma unroll
-                for (int ks = 0; ks < kPtKeys / 16; ++ks)
-                    umma_ts(tmem + kPtO + 128u * t, pcol + 8 * ks, umma_desc_lbo(vb + 2048 * ks, kPtHalf), IDESC_PV,
-                            (acc || ks > 0) ? 1u : 0u);
-            };
-            do {
-                const int nt = w.x.ntok > a.tb ? 2 : 1;
-                const int n = w.n;
-                for (int t = 0; t < nt && ok; ++t) {
-                    wait(&q_ready[t], n_q[t] & 1u);
-                    if (t == 0) wait(&full[e % NST], (unsigned)(e / NST) & 1u);
-                    if (ok) issue_s(t, e);
-                }
-                if (ok) umma_commit(&empty[e % NST]);
-                for (int i = 0; ok && i < n; ++i) {
-                    const int ek = e + 2 * (i + 1), ev = e + 2 * i + 1;
-                    for (int t = 0; t < nt && ok; ++t) {
-                        if (t == 0) wait(&v_ready[ev % NST], (unsigned)((ev / NST) >> 1) & 1u);
-                        if (i == 0) wait(&o_empty[t], (n_q[t] & 1u) ^ 1u);
-                        wait(&p_full[t], n_p[t] & 1u);
+                for (int ks = 0; ks < kPtKeys / 32; ++ks)
+                    umma_ts(d, pcol + 8 * ks, dv + ks * (2048 >> 4), IDESC_PV, (acc || ks > 0) ? 1u : 0u);
+                umma_commit(&pv_done[t]);
+            }
+        };
+        // a stage on: NST is odd, so K and V alternate on every stage
+        auto step = [&](int &stage, unsigned &lap) {
+            stage += 2;
+            if (stage >= NST) {
+                stage -= NST;
+                ++lap;
+            }
+        };
+        do {
+            const int nt = __shfl_sync(0xffffffffu, w.x.ntok > a.tb ? 2 : 1, 0);
+            const int n = __shfl_sync(0xffffffffu, w.n, 0);
+            wait(&full[sk], lk);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t >= nt) break;
+                wait(&q_ready[t], n_q[t]);
+                if (ok) issue_s(t, 0), issue_s(t, 1);
+            }
+            if (ok) commit(&empty[sk]);
+            step(sk, lk);
+            for (int i = 0; ok && i < n; ++i) {
+                wait(&v_ready[sv], lv >> 1);
+                if (i < n - 1) wait(&full[sk], lk);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= nt) break;
+                        if (i == 0 && h == 0) wait(&o_empty[t], n_q[t] ^ 1u);
+                        wait(&p_full[2 * t + h], n_p[t]);
                         if (!ok) break;
-                        ++n_p[t];
-                        issue_pv(t, ev, i > 0);
-                        if (t == nt - 1) umma_commit(&empty[ev % NST]);
-                        if (i == n - 1) {
-                            umma_commit(&o_full[t]);
-                        } else {
-                            if (t == 0) wait(&full[ek % NST], (unsigned)(ek / NST) & 1u);
-                            if (!ok) break;
-                            issue_s(t, ek);
-                            if (t == nt - 1) umma_commit(&empty[ek % NST]);
-                        }
+                        issue_pv(t, h, i > 0 || h > 0);
+                        if (i < n - 1) issue_s(t, h);
+                        else if (h == 1) commit(&o_full[t]);
                     }
+                if (!ok) break;
+                commit(&empty[sv]);
+                ++n_p[0];
+                if (nt == 2) ++n_p[1];
+                step(sv, lv);
+                if (i < n - 1) {
+                    commit(&empty[sk]);
+                    step(sk, lk);
                 }
-                e += 2 * n;
-                for (int t = 0; t < nt; ++t) ++n_q[t];
-            } while (ok && w.next(a));
-            if (!ok) *s_fail = 1;
-            umma_commit(fin);
-            if (!mbar_wait(fin, 0)) *s_fail = 1;
-        }
+            }
+            ++n_q[0];
+            if (nt == 2) ++n_q[1];
+        } while (ok && __shfl_sync(0xffffffffu, (int)w.next(a), 0));
+        if (!ok) *s_fail = 1;
+        commit(fin);
+        if (!mbar_wait(fin, 0)) *s_fail = 1;
     } else if (busy && warp == 2) {
         // ---- values of keys that no row sees become zero ----
         int e = 1;
@@ -557,7 +592,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         const int r = 32 * qd + lane;
         const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
         const uint32_t scol = tmem + lane_off + kPtS + 128u * t, ocol = tmem + lane_off + kPtO + 128u * t;
-        unsigned n_s = 0, seg = 0;  // phases
+        unsigned n_s = 0, seg = 0;  // half tiles (phases of s_full and pv_done) and segments so far
         bool ok = true;
         do {
             const PtItem &x = w.x;
@@ -611,39 +646,36 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                 if (lane == 0) mbar_arrive(&q_ready[t]);
             }
             float m = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
-            for (int i = 0; i < w.n; ++i) {
-                ok = __all_sync(0xffffffffu, !*s_fail && mbar_wait(&s_full[t], n_s & 1u));
+#pragma unroll 1
+            for (int i = 0; i < 2 * w.n; ++i) {
+                const int h = i & 1;
+                const uint32_t hcol = scol + 64u * h;
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * t + h], (n_s >> 1) & 1u));
                 if (!ok) break;
                 ++n_s;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 if (warp_live) {
-                    const int k0 = x.tile(w.i0 + i) * kPtKeys;
-                    const bool all = k0 + kPtKeys - 1 <= all_p && (k0 >= all_lo || k0 + kPtKeys <= a.sinks);
-                    auto mask = [&](float *s, int key0) {  // 32 logits from key key0
-                        if (all) return;
-                        // key <= p && (key >= lo || key < sinks), a bit per key
-                        const uint32_t vis = low_bits(p - key0 + 1) & (~low_bits(lo - key0) | low_bits(a.sinks - key0));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(vis >> e & 1u)) s[e] = -INFINITY;
-                    };
-                    // the maximum first; the row's second half stays in registers, the first
-                    // is loaded again for its exponentials
+                    const int k0 = x.tile(w.i0 + (i >> 1)) * kPtKeys + 64 * h;
                     float s[64], mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_ld32(hcol, s);
+                    tmem_ld32(hcol + 32, s + 32);
+                    tmem_ld_wait();
+                    tmem_ld_done(s);
+                    tmem_ld_done(s + 32);
+                    if (!(k0 + 63 <= all_p && (k0 >= all_lo || k0 + 64 <= a.sinks))) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tmem_ld32(scol + 64 * h, s);
-                        tmem_ld32(scol + 64 * h + 32, s + 32);
-                        tmem_ld_wait();
-                        tmem_ld_done(s);
-                        tmem_ld_done(s + 32);
-                        mask(s, k0 + 64 * h);
-                        mask(s + 32, k0 + 64 * h + 32);
+                        for (int c = 0; c < 2; ++c) {
+                            const int kc = k0 + 32 * c;  // key <= p && (key >= lo || key < sinks), a bit per key
+                            const uint32_t vis = low_bits(p - kc + 1) & (~low_bits(lo - kc) | low_bits(a.sinks - kc));
 #pragma unroll
-                        for (int e = 0; e < 64; e += 8)  // four chains: one would be latency
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) mc[c] = max3(mc[c], s[e + c], s[e + 4 + c]);
+                            for (int e = 0; e < 32; ++e)
+                                if (!(vis >> e & 1u)) s[32 * c + e] = -INFINITY;
+                        }
                     }
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8)  // four chains: one would be latency
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) mc[c] = max3(mc[c], s[e + c], s[e + 4 + c]);
                     const float mx = max3(fmaxf(mc[0], mc[1]), mc[2], mc[3]) * a.scale_log2;
                     // raise the running maximum only when this tile exceeds it by > 8
                     const bool need = mx > m + kAmLazy;
@@ -651,7 +683,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                         const float mn = need ? mx : m;
                         const float f = need ? exp2f(m - mn) : 1.f;  // 0 on the first step (m = -inf)
                         if (i > 0) {
-                            // S of this tile was committed after the last P V of this row, so O is at rest
+                            // the product of the half tile before may still be adding to O
+                            // (n_s counts this one: phase n_s - 2)
+                            if (!__all_sync(0xffffffffu, !*s_fail && mbar_wait(&pv_done[t], n_s & 1u))) *s_fail = 1;
+                            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
                             for (int c = 0; c < 8; ++c) {
                                 float v[16];
@@ -668,33 +703,20 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                     const float sub = m == -INFINITY ? 0.f : m;  // no key seen yet: every term is 2^-inf
                     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), sub2 = pack2(-sub, -sub);
                     uint64_t l2[2] = {0, 0};
-                    // P (bf16) replaces the row's second half: keys 0-63, then 64-127
-                    auto exps = [&](const float *v, int chunk) {
+                    // P (bf16) replaces the first 32 of these 64 columns
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t u[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float x0, x1;
-                            unpack2(fma2(pack2(v[2 * e], v[2 * e + 1]), scale2, sub2), x0, x1);
+                            unpack2(fma2(pack2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), scale2, sub2), x0, x1);
                             const float p0 = ex2(x0), p1 = ex2(x1);
                             l2[e & 1] = add2(l2[e & 1], pack2(p0, p1));
                             u[e] = pack_bf16x2(p0, p1);
                         }
-                        tmem_st16(scol + 64 + 16 * chunk, u);
-                    };
-                    float r0[32];
-                    tmem_ld32(scol, r0);
-                    exps(s, 2);
-                    exps(s + 32, 3);
-                    tmem_ld_wait();
-                    tmem_ld_done(r0);
-                    mask(r0, k0);
-                    float r1[32];
-                    tmem_ld32(scol + 32, r1);
-                    exps(r0, 0);
-                    tmem_ld_wait();
-                    tmem_ld_done(r1);
-                    mask(r1, k0 + 32);
-                    exps(r1, 1);
+                        tmem_st16(hcol + 16 * c, u);
+                    }
                     float l0, l1;
                     unpack2(add2(l2[0], l2[1]), l0, l1);
                     l += l0 + l1;
@@ -702,7 +724,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
+                if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
             }
             if (!ok) break;
             ok = __all_sync(0xffffffffu, !*s_fail && mbar_wait(&o_full[t], seg & 1u));
