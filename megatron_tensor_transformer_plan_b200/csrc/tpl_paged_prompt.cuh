@@ -13,18 +13,18 @@
 // unnormalised output) per CTA in the workspace; a second kernel joins them.
 // Neighbouring CTAs work on the same kv head, so its keys come from L2.
 //
-// 20 warps:
-//   0, 3  TMA producers of the K and of the V tiles, in turn into a ring, a lane
-//         per page part (64 dims of at most 128 keys of one page), no multicast;
-//   1     TMEM owner and MMA issuer (one thread);
+// 12 warps:
+//   0     TMA producer: K and V tiles in turn into a ring, a lane per page
+//         part (64 dims of at most 128 keys of one page), no multicast;
+//   1, 3  MMA issuers of tile 0 and of tile 1 (warp 1 owns the tensor memory);
 //   2     replaces the values of keys that no row sees by zero (0 * NaN is NaN)
 //         in the tiles that have such keys, before the MMA reads them;
-//   4-11  softmax of tile 0, 12-19 softmax of tile 1: two threads per row, 64 of
-//         a tile's 128 keys each.  They share the row's maximum through shared
-//         memory; four warps per scheduler hide one another's latencies.
+//   4-7   softmax of tile 0, 8-11 softmax of tile 1: one thread per row.
+// A key tile is taken in two halves of 64 keys: S of one half is formed while
+// the softmax works on the other, and the two tiles alternate, so that neither
+// the tensor cores nor the special-function units wait for a round trip.
 // S = Q K^T reads Q (bf16, or bf16 hi + lo when q is fp32: two products) and K
-// from shared memory; P replaces half of S in tensor memory as bf16; O += P V.  The
-// two tiles alternate, so the MMAs of one run under the softmax of the other.
+// from shared memory; P replaces half of S in tensor memory as bf16; O += P V.
 // P has one bf16 part: with o rounded to bf16 anyway, the two roundings are of
 // the same size (2^-9 of each term against 2^-9 of the sum); the denominator
 // adds the unrounded fp32 terms.
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
     volatile int *s_fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_issued = const_cast<int *>(s_fail) + 1;
-    int *s_where = s_issued + 2;          // [4] start of this CTA's range: j, b, item, tiles before
+    int *s_where = s_issued + 1;          // [4] start of this CTA's range: j, b, item, tiles before
     long long *s_sum = reinterpret_cast<long long *>((reinterpret_cast<uintptr_t>(s_where + 4) + 7) & ~(uintptr_t)7);
     static_assert((3 * NST + 17) * 8 + 40 + 16 + kPtThreads / 32 * 8 <= SM::BAR, "barrier area");
 
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);
             mbar_init(&v_ready[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -278,9 +278,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             mbar_init(&o_full[t], 1);
             mbar_init(&o_empty[t], 4);
         }
-        mbar_init(fin, 1);
+        mbar_init(fin, 2);
         *s_fail = 0;
-        s_issued[0] = s_issued[1] = 0;
+        *s_issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -408,15 +408,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         w.open(a);
     }
 
-    if (busy && (warp == 0 || warp == 3)) {
-        // ---- TMA producers: warp 0 the keys (even ring elements), warp 3 the values.
-        //      The pages of 32 parts (whole tiles) are looked up at once, a batch ahead. ----
-        const int kv = warp == 0 ? 0 : 1;
+    if (busy && warp == 0) {
+        // ---- TMA producer: K and V tiles in turn.  The pages of 32 parts (whole tiles)
+        //      are looked up at once, a batch ahead. ----
         const int box_shift = min(a.v.page_shift, 7);
         const int nsub = kPtKeys >> box_shift;  // parts of a tile: at most 8
         const int half = lane / nsub, sub = lane % nsub;  // this lane's copy (half < 2)
         const int batch = 32 / nsub;            // tiles per lookup
-        int e = kv;
+        int e = 0;
         bool ok = true;
         do {
             const PtItem &x = w.x;
@@ -439,69 +438,74 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                     page = 0;
                 }
                 const int base = page < 0 ? -1 : (int)((jrow + (int64_t)page * a.v.nkv_s) << a.v.page_shift);
-                for (int i = ib; ok && i < min(ib + batch, i1); ++i, e += 2) {
+                for (int i = ib; ok && i < min(ib + batch, i1); ++i) {
                     int row = __shfl_sync(0xffffffffu, base, (i - ib) * nsub + sub);
                     const bool want = half < 2 && row >= 0;
                     row += (x.tile(i) * kPtKeys + (sub << box_shift)) & ((1 << a.v.page_shift) - 1);
                     const unsigned bytes = (unsigned)__popc(__ballot_sync(0xffffffffu, want)) << (box_shift + 7);
-                    const int s = e % NST;
-                    bool go = true;
-                    if (lane == 0) {
-                        go = !*s_fail && mbar_wait(&empty[s], ((unsigned)(e / NST) & 1u) ^ 1u);
-                        if (go) mbar_expect_tx(&full[s], bytes);
+                    for (int kv = 0; ok && kv < 2; ++kv) {
+                        const int s = e % NST;
+                        bool go = true;
+                        if (lane == 0) {
+                            go = mbar_wait(&empty[s], ((unsigned)(e / NST) & 1u) ^ 1u);
+                            if (go) mbar_expect_tx(&full[s], bytes);
+                        }
+                        ok = __all_sync(0xffffffffu, go);
+                        if (!ok) break;
+                        if (want)
+                            tma_load_2d(ring + s * kPtTile + half * kPtHalf + (sub << (box_shift + 7)),
+                                        kv ? &a.tm_v : &a.tm_k, 64 * half, row, &full[s]);
+                        ++e;
                     }
-                    ok = __all_sync(0xffffffffu, go);
-                    if (!ok) break;
-                    if (want)
-                        tma_load_2d(ring + s * kPtTile + half * kPtHalf + (sub << (box_shift + 7)),
-                                    kv ? &a.tm_v : &a.tm_k, 64 * half, row, &full[s]);
                 }
             }
         } while (ok && w.next(a));
         if (!ok) *s_fail = 1;
-        if (lane == 0) s_issued[kv] = e;
-    } else if (busy && warp == 1) {
-        // The whole warp walks, one elected lane issues: what the products take
-        // (addresses, descriptors) is then warp-uniform and stays in uniform
-        // registers.  Issued from a branch of one lane, every product waited
-        // about 100 cycles for its operands to be moved there.
+        if (lane == 0) *s_issued = e;
+    } else if (busy && (warp == 1 || warp == 3)) {
+        // ---- MMA issuers: warp 1 the products of tile 0, warp 3 those of tile 1.  The whole
+        //      warp walks and one elected lane issues, so that the products' operands stay
+        //      in uniform registers. ----
+        const int t = warp >> 1;
         constexpr uint32_t IDESC_S = umma_idesc(128, kPtKeys / 2);
         constexpr uint32_t IDESC_PV = umma_idesc(128, 128) | (1u << 16);  // B (V) MN-major
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t dq = umma_desc(smem_u32(s_q)), dk0 = umma_desc(smem_u32(ring)),
-                       dv0 = umma_desc_lbo(smem_u32(ring), kPtHalf);
         constexpr unsigned TILE16 = kPtTile >> 4, HALF16 = kPtHalf >> 4, ROWS16 = 64 * 128 >> 4;  // (descriptors count 16 bytes)
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = umma_desc(smem_u32(s_q)) + t * SM::QPARTS * TILE16, dk0 = umma_desc(smem_u32(ring)),
+                       dv0 = umma_desc_lbo(smem_u32(ring), kPtHalf);
+        const uint32_t d_o = tm + kPtO + 128u * t, d_s = tm + kPtS + 128u * t;
         int sk = 0, sv = 1;                // ring stages of the next K and V
         unsigned lk = 0, lv = 0;           // and their laps (v_ready has a phase per two laps)
-        unsigned n_p[2] = {0, 0}, n_q[2] = {0, 0};  // phases of p_full, and of q_ready / o_empty
+        unsigned n_p = 0, n_q = 0;         // phases of p_full, and of q_ready / o_empty
         bool ok = true;
         auto wait = [&](uint64_t *bar, unsigned parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
         auto commit = [&](uint64_t *bar) {
             if (elect_one()) umma_commit(bar);
         };
-        auto issue_s = [&](int t, int h) {  // 64 keys of S_t = Q_t K^T
-            const uint64_t dk = dk0 + sk * TILE16 + h * ROWS16, da = dq + t * SM::QPARTS * TILE16;
-            const uint32_t d = tm + kPtS + 128u * t + 64u * h;
+        auto issue_s = [&](int h) {  // 64 keys of S = Q K^T
+            const uint64_t dk = dk0 + sk * TILE16 + h * ROWS16;
             if (elect_one()) {
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     const unsigned off = (kk >> 2) * HALF16 + 2 * (kk & 3);
-                    umma(d, da + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
-                    if (QF32) umma(d, da + TILE16 + off, dk + off, IDESC_S, 1u);
+                    umma(d_s + 64u * h, dq + off, dk + off, IDESC_S, kk > 0 ? 1u : 0u);
+                    if (QF32) umma(d_s + 64u * h, dq + TILE16 + off, dk + off, IDESC_S, 1u);
                 }
                 umma_commit(&s_full[2 * t + h]);
+                if (h == 1) umma_commit(&empty[sk]);
             }
         };
-        auto issue_pv = [&](int t, int h, bool acc) {  // O_t += P_t V over 64 keys
+        auto issue_pv = [&](int h, bool acc, bool last) {  // O += P V over 64 keys
             const uint64_t dv = dv0 + sv * TILE16 + h * ROWS16;
-            const uint32_t pcol = tm + kPtS + 128u * t + 64u * h, d = tm + kPtO + 128u * t;
             if (elect_one()) {
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
                 for (int ks = 0; ks < kPtKeys / 32; ++ks)
-                    umma_ts(d, pcol + 8 * ks, dv + ks * (2048 >> 4), IDESC_PV, (acc || ks > 0) ? 1u : 0u);
+                    umma_ts(d_o, d_s + 64u * h + 8 * ks, dv + ks * (2048 >> 4), IDESC_PV, (acc || ks > 0) ? 1u : 0u);
                 umma_commit(&pv_done[t]);
+                if (h == 1) umma_commit(&empty[sv]);
+                if (h == 1 && last) umma_commit(&o_full[t]);
             }
         };
         // a stage on: NST is odd, so K and V alternate on every stage
@@ -513,44 +517,35 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             }
         };
         do {
-            const int nt = __shfl_sync(0xffffffffu, w.x.ntok > a.tb ? 2 : 1, 0);
+            const bool mine = __shfl_sync(0xffffffffu, (int)(t == 0 || w.x.ntok > a.tb), 0);
             const int n = __shfl_sync(0xffffffffu, w.n, 0);
+            if (mine) wait(&q_ready[t], n_q);
             wait(&full[sk], lk);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (t >= nt) break;
-                wait(&q_ready[t], n_q[t]);
-                if (ok) issue_s(t, 0), issue_s(t, 1);
-            }
-            if (ok) commit(&empty[sk]);
+            if (ok && mine) issue_s(0), issue_s(1);
+            if (ok && !mine) commit(&empty[sk]);  // (an item of one tile: its stages need this warp's word too)
             step(sk, lk);
             for (int i = 0; ok && i < n; ++i) {
+                const bool more = i < n - 1;
                 wait(&v_ready[sv], lv >> 1);
-                if (i < n - 1) wait(&full[sk], lk);
+                if (more) wait(&full[sk], lk);
+                if (mine) {
+                    if (i == 0) wait(&o_empty[t], n_q ^ 1u);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t >= nt) break;
-                        if (i == 0 && h == 0) wait(&o_empty[t], n_q[t] ^ 1u);
-                        wait(&p_full[2 * t + h], n_p[t]);
+                    for (int h = 0; h < 2; ++h) {
+                        wait(&p_full[2 * t + h], n_p);
                         if (!ok) break;
-                        issue_pv(t, h, i > 0 || h > 0);
-                        if (i < n - 1) issue_s(t, h);
-                        else if (h == 1) commit(&o_full[t]);
+                        issue_pv(h, i > 0 || h > 0, !more);
+                        if (more) issue_s(h);
                     }
-                if (!ok) break;
-                commit(&empty[sv]);
-                ++n_p[0];
-                if (nt == 2) ++n_p[1];
-                step(sv, lv);
-                if (i < n - 1) {
-                    commit(&empty[sk]);
-                    step(sk, lk);
+                    ++n_p;
+                } else if (ok) {
+                    commit(&empty[sv]);
+                    if (more) commit(&empty[sk]);
                 }
+                step(sv, lv);
+                if (more) step(sk, lk);
             }
-            ++n_q[0];
-            if (nt == 2) ++n_q[1];
+            if (mine) ++n_q;
         } while (ok && __shfl_sync(0xffffffffu, (int)w.next(a), 0));
         if (!ok) *s_fail = 1;
         commit(fin);
@@ -780,9 +775,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     __syncthreads();
     if (*s_fail && threadIdx.x == 0) {
         record_error(8u);
-        for (int kv = 0; kv < 2; ++kv)  // the copies in flight: the last of the ring's laps
-            for (int e = s_issued[kv] - 2; e >= 0 && e >= s_issued[kv] - 2 * NST; e -= 2)
-                mbar_wait(&full[e % NST], (unsigned)(e / NST) & 1u);
+        const int e1 = *s_issued;
+        for (int e = e1 > NST ? e1 - NST : 0; e < e1; ++e) mbar_wait(&full[e % NST], (unsigned)(e / NST) & 1u);
     }
     __syncthreads();
     if (warp == 1) {
