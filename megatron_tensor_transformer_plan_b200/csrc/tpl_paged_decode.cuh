@@ -16,13 +16,18 @@
 // unnormalised output) and the last of its CTAs to arrive joins them in CTA
 // order, so results do not depend on the timing.
 //
-// Per CTA one warp issues the TMA copies (a lane per page part: 64 dimensions
-// of at most 64 keys of one page) into a ring of stages of 64 keys; two groups
+// Per CTA: one producer warp issues the TMA copies (a lane per page part: all
+// 128 dimensions of at most 64 keys of one page) into a ring of stages of 64
+// keys; it looks the pages of 32 parts up at once, a batch ahead.  Two groups
 // of four warps take alternate stages, 16 keys per warp, on mma.sync m16n8k16:
 // the queries are carried as bf16 hi + lo parts (q is fp32: together 16 bits of
 // mantissa), as is P, so the bf16 cache is the only rounding of the products.
 // With g <= 8 the two parts are rows 0-7 and 8-15 of one product; with g up to
 // 16 they are two products.  tcgen05 would pad the g rows to 128.
+// At the end of a pair the eight warps leave their states in shared memory and
+// go on; two merging warps join them, write the result and bring the queries
+// of the pair after next, so that short sequences do not wait on each other's
+// ends (64 sequences of 130 to 512 keys behind a prefix: 72 us without them).
 //
 // A page none of whose keys is visible is not read, nor is its table entry;
 // keys that are not visible are masked by a select and their values replaced
@@ -39,25 +44,32 @@ namespace tpl {
 constexpr int kPdKeys = 64;                       // keys per stage
 constexpr int kPdBox = kPdKeys * 128;             // 64 keys x 64 dims, bf16: 8 KB
 constexpr int kPdStage = 4 * kPdBox;              // K low and high dims, V low and high dims
-constexpr int kPdThreads = kAmThreads;            // 8 consumer warps and the producer
+constexpr int kPdMergeWarp = kAmWarps + 1;        // first merging warp, behind the producer
+constexpr int kPdMergeWarps = 2;
+constexpr int kPdThreads = (kPdMergeWarp + kPdMergeWarps) * 32;  // 8 consumer warps, the producer, the merging warps
 constexpr int kPdMinBlocks = 2;                   // blocks per CTA at least
+constexpr int kPdRow = 136;                       // floats between the rows of a state: 8 rows apart in banks
 
 template <int GM>
 struct PdSmem {
-    static constexpr int NS = GM == 8 ? 6 : 4;
+    static constexpr int NS = 4;
     // a stage belongs to one group: its parity names a lap only to a reader
     // that has seen the lap before land
     static_assert(NS % kAmGroups == 0, "stages per group");
-    static constexpr int MERGE = kAmGroupWarps * GM * 128 * 4;
-    static constexpr int BAR = 3072;
+    static constexpr int SLOTS = GM == 8 ? 2 : 1;              // states of finished pairs
+    static constexpr int STATE = kAmWarps * GM * kPdRow * 4;   // [8 warps][GM][kPdRow]
+    static constexpr int ML = kAmWarps * GM * 8;               // [8 warps][GM](max, sum)
+    static constexpr int Q = 2 * GM * 256;                     // hi rows, lo rows; two pairs
+    static constexpr int JOIN = kAmWarps * GM * 4 + 2 * GM * 4;  // the merge's weights, maxima and sums
+    static constexpr int BAR = 512;
     static constexpr int SCAN = (kPagedMaxSeqs + 1) * 8;
-    static constexpr size_t BYTES = (size_t)NS * kPdStage + MERGE + BAR + SCAN + 1024;
+    static constexpr size_t BYTES = (size_t)NS * kPdStage + 2 * Q + SLOTS * (STATE + ML) + JOIN + BAR + SCAN + 1024;
     static_assert(BYTES <= 232448, "shared memory per block");
-    static_assert(kPagedMaxCtas * GM * 3 * 4 <= MERGE, "the join's tables");
+    static_assert(kPagedMaxCtas * GM * 3 * 4 <= STATE, "the join's tables");
 };
 
 struct PagedDecodeArgs {
-    CUtensorMap tm_k, tm_v;  // pool rows x 128, boxes of 64 dims x min(64, page) rows
+    CUtensorMap tm_k, tm_v;  // 64 dims x pool rows x 2 halves, boxes of 64 x min(64, page) x 2
     PagedView v;
     const void *q;           // [n_seqs] rows
     int q_f32;
@@ -97,23 +109,47 @@ __device__ __forceinline__ PdSpan pd_span(const PagedDecodeArgs &a, int len) {
     return s;
 }
 
+// (sequence, kv head, block) of the units in order.
+struct PdWalk {
+    int b, j;
+    PdSpan sp;
+    __device__ __forceinline__ void open(const PagedDecodeArgs &a, int b_) {
+        b = b_;
+        sp = pd_span(a, paged_len(a.v, b));
+    }
+    // the next pair
+    __device__ __forceinline__ void next(const PagedDecodeArgs &a, const long long *start) {
+        if (++j == a.v.nkv) {
+            j = 0;
+            do ++b;
+            while (start[b + 1] == start[b]);
+            open(a, b);
+        }
+    }
+};
+
 template <int GM>
 __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int D = 128;
     using SM = PdSmem<GM>;
-    constexpr int NS = SM::NS;
+    constexpr int NS = SM::NS, NB = SM::SLOTS;
     constexpr int RPT = GM / 8;  // rows (heads) per thread
     extern __shared__ __align__(1024) unsigned char pd_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)pd_raw + 1023) & ~(uintptr_t)1023);
-    float *s_o = reinterpret_cast<float *>(sm + NS * kPdStage);  // [4 warps][GM][128]
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + NS * kPdStage + SM::MERGE);
+    unsigned char *s_q = sm + NS * kPdStage;                                   // [2][hi, lo][GM][256 B], swizzled
+    float *s_o = reinterpret_cast<float *>(s_q + 2 * SM::Q);                   // [NB][8 warps][GM][kPdRow]
+    float *s_ml = s_o + NB * SM::STATE / 4;                                    // [NB][8 warps][GM][2]
+    float *s_wt = s_ml + NB * SM::ML / 4;                                      // [8 warps][GM]
+    float *s_M = s_wt + kAmWarps * GM, *s_den = s_M + GM;
+    uint64_t *full = reinterpret_cast<uint64_t *>(s_den + GM);
     uint64_t *empty = full + NS;
-    float *s_ml = reinterpret_cast<float *>(empty + NS);  // [4 warps][GM][2]
-    float *s_misc = s_ml + kAmGroupWarps * GM * 2;        // M[GM], den[GM]
-    long long *s_warp = reinterpret_cast<long long *>(s_misc + 2 * GM);  // [warps]
-    volatile int *s_flag = reinterpret_cast<volatile int *>(s_warp + 16);  // fail, last, issued
-    static_assert(2 * NS * 8 + (kAmGroupWarps * GM * 2 + 2 * GM) * 4 + 16 * 8 + 16 <= SM::BAR, "barrier area");
-    long long *s_start = reinterpret_cast<long long *>(sm + NS * kPdStage + SM::MERGE + SM::BAR);  // [n_seqs + 1]
+    uint64_t *q_full = empty + NS;     // [2]
+    uint64_t *st_full = q_full + 2;    // [NB]
+    uint64_t *st_empty = st_full + NB; // [NB]
+    volatile int *s_flag = reinterpret_cast<volatile int *>(st_empty + NB);  // fail, last, issued
+    long long *s_warp = reinterpret_cast<long long *>(st_empty + NB + 2);    // [warps]
+    static_assert((2 * NS + 2 + 2 * NB + 2 + kPdThreads / 32) * 8 <= SM::BAR, "barrier area");
+    long long *s_start = reinterpret_cast<long long *>(reinterpret_cast<unsigned char *>(full) + SM::BAR);  // [n_seqs + 1]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
@@ -122,6 +158,11 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kAmGroupWarps);
+        }
+        for (int s = 0; s < 2; ++s) mbar_init(&q_full[s], kPdMergeWarps);
+        for (int s = 0; s < NB; ++s) {
+            mbar_init(&st_full[s], kAmWarps);
+            mbar_init(&st_empty[s], kPdMergeWarps);
         }
         s_flag[0] = 0;
         s_flag[1] = 0;
@@ -184,130 +225,97 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
 
     const int64_t u0 = am_start(U, G, cta), u1 = am_start(U, G, cta + 1);
     const int n = (int)(u1 - u0);
-    int b0;  // the sequence of unit u0
-    {
-        int l = 0, r = v.n_seqs - 1;  // the last b with s_start[b] <= u0 that is not empty
+    // the sequence of unit u: the last one that begins at or before it
+    auto seq_of = [&](int64_t u) {
+        int l = 0, r = v.n_seqs - 1;
         while (l < r) {
             const int mid = (l + r + 1) >> 1;
-            if (s_start[mid] <= u0) l = mid;
+            if (s_start[mid] <= u) l = mid;
             else r = mid - 1;
         }
-        b0 = l;
-    }
+        return l;
+    };
     const int box_shift = min(v.page_shift, 6);  // rows per copy
 
     if (warp == kAmWarps) {
-        // ---- producer: lane = (part, page part) ----
+        // ---- producer: lane = (K or V, page part) ----
         const uint64_t kvpol = evict_first_policy();
-        const int nsub = kPdKeys >> box_shift;  // copies per part
-        const int part = lane / nsub, sub = lane % nsub;
-        const bool active = part < 4;
-        int b = b0;
-        PdSpan sp = pd_span(a, paged_len(v, b));
-        int64_t rel = u0 - s_start[b];
-        int j = (int)(rel / sp.nblk), blk = (int)(rel % sp.nblk);
-        // this lane's copy of the current unit: its key, whether any of it is visible, its pool row
-        auto place = [&](bool &want, int &row) {
-            const int key = sp.block(blk) * kPdKeys + (sub << box_shift);
-            const int end = key + (1 << box_shift);
-            want = active && key < sp.len && (end > sp.lo || key < sp.sk);
-            row = 0;
-            if (want) {
-                const int64_t r = paged_row(v, b, key >> v.page_shift, j);
-                row = r < 0 ? 0 : (int)r + (key & ((1 << v.page_shift) - 1));
-            }
+        const int nsub = kPdKeys >> box_shift;  // parts of a block: 1, 2 or 4
+        const int batch = 32 / nsub;            // blocks per lookup
+        const int kv = lane / nsub, sub = lane % nsub;
+        // the pool row of part lane % nsub of unit i0 + lane / nsub, -1 when no key of it is seen
+        auto lookup = [&](int i0) {
+            const int i = min(i0 + lane / nsub, n - 1);
+            const int64_t u = u0 + i;
+            PdWalk w;
+            w.open(a, seq_of(u));
+            const int64_t rel = u - s_start[w.b];
+            w.j = (int)(rel / w.sp.nblk);
+            const int key = w.sp.block((int)(rel - (int64_t)w.j * w.sp.nblk)) * kPdKeys + ((lane % nsub) << box_shift);
+            const bool want = i0 + lane / nsub < n && key < w.sp.len && (key + (1 << box_shift) > w.sp.lo || key < w.sp.sk);
+            if (!want) return -1;
+            const int64_t r = paged_row(v, w.b, key >> v.page_shift, w.j);
+            return r < 0 ? 0 : (int)r + (key & ((1 << v.page_shift) - 1));
         };
-        bool want;
-        int row;
-        place(want, row);
+        int ahead = lookup(0);
+        bool ok = true;
         int i = 0;
-        for (; i < n; ++i) {
-            const int s = i % NS;
-            bool ok = true;
-            if (lane == 0 && i >= NS) ok = !s_flag[0] && mbar_wait(&empty[s], ((unsigned)(i / NS) & 1u) ^ 1u);
-            if (!__all_sync(0xffffffffu, ok)) {
-                s_flag[0] = 1;
-                break;
-            }
-            const unsigned ballot = __ballot_sync(0xffffffffu, want);
-            if (lane == 0) mbar_expect_tx(&full[s], (unsigned)__popc(ballot) << (box_shift + 7));
-            __syncwarp();
-            if (want)
-                tma_load_2d_hint(sm + s * kPdStage + part * kPdBox + (sub << (box_shift + 7)),
-                                 part < 2 ? &a.tm_k : &a.tm_v, 64 * (part & 1), row, &full[s], kvpol);
-            if (i + 1 < n) {  // the next unit's page is looked up while this one's copies fly
-                if (++blk == sp.nblk) {
-                    blk = 0;
-                    if (++j == v.nkv) {
-                        j = 0;
-                        do ++b;
-                        while (s_start[b + 1] == s_start[b]);
-                        sp = pd_span(a, paged_len(v, b));
-                    }
+        for (int ib = 0; ok && ib < n; ib += batch) {
+            const int rows = ahead;
+            if (ib + batch < n) ahead = lookup(ib + batch);
+            for (; i < min(ib + batch, n); ++i) {
+                const int s = i % NS;
+                const int row = __shfl_sync(0xffffffffu, rows, (i - ib) * nsub + sub);
+                const bool want = kv < 2 && row >= 0;
+                const unsigned bytes = (unsigned)__popc(__ballot_sync(0xffffffffu, want)) << (box_shift + 8);
+                if (lane == 0) {
+                    ok = !s_flag[0] && mbar_wait(&empty[s], ((unsigned)(i / NS) & 1u) ^ 1u);
+                    if (ok) mbar_expect_tx(&full[s], bytes);
                 }
-                place(want, row);
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+                if (!ok) break;
+                if (want)
+                    tma_load_3d_hint(sm + s * kPdStage + kv * 2 * kPdBox + (sub << (box_shift + 8)),
+                                     kv ? &a.tm_v : &a.tm_k, 0, row, 0, &full[s], kvpol);
             }
         }
+        if (!ok) s_flag[0] = 1;
         if (lane == 0) s_flag[2] = i;
-    } else {
+    } else if (warp < kAmWarps) {
         // ---- consumers: group grp takes the stages i with i % kAmGroups == grp ----
         const int gid = lane >> 2, c = lane & 3;
         const int grp = warp / kAmGroupWarps, wl = warp % kAmGroupWarps;
-        const int tid = threadIdx.x;  // group 0: 0..127, one head dimension each in the merge
-        bool dead = false;
-        int i = 0;
-        int b = b0;
-        PdSpan sp = pd_span(a, paged_len(v, b));
-        int64_t pair_start = s_start[b];
-        int j = 0;
+        bool dead = false;  // after a timeout the warps walk on without waiting, so that every barrier still meets
+        // this warp's 16 keys of a stage: their rows in the part's box, the two halves of the dims
+        const unsigned half_bytes = 1u << (box_shift + 7);
+        const int row_in = (16 * wl) & ((1 << box_shift) - 1);
+        const unsigned part_off = (unsigned)((16 * wl) >> box_shift) * 2 * half_bytes;
+        PdWalk w;
+        w.open(a, seq_of(u0));
+        int64_t pair_start = s_start[w.b];
         {
             const int64_t rel = u0 - pair_start;
-            j = (int)(rel / sp.nblk);
-            pair_start += (int64_t)j * sp.nblk;
+            w.j = (int)(rel / w.sp.nblk);
+            pair_start += (int64_t)w.j * w.sp.nblk;
         }
-        while (i < n) {
+        int i = 0;
+        for (int seg = 0; i < n; ++seg) {
             // one segment: the blocks of one pair
+            const PdSpan &sp = w.sp;
             const int64_t pair_end = pair_start + sp.nblk;
             const int first = (int)(u0 + i - pair_start);
             const int seg_n = (int)(min(u1, pair_end) - (u0 + i));
-            // q fragments: row r = head, dims 16 ks + 2c (+1, +8, +9); hi and lo parts
-            uint32_t qf[8][4], ql[RPT == 2 ? 8 : 1][4];
+            // q fragments of the hi parts (GM == 8: rows 8-15 are the lo parts)
+            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&q_full[seg & 1], (unsigned)(seg >> 1) & 1u));
+            const unsigned char *q = s_q + (seg & 1) * SM::Q;
+            const int q_row = (lane & 7) + ((lane >> 3 & 1) << 3), q_chunk = lane >> 4;
+            auto q_frag = [&](int part, int ks, uint32_t (&f)[4]) {
+                const int row = 16 * part + q_row;
+                ldsm_x4(q + row * 256 + (((2 * ks + q_chunk) ^ (row & 7)) << 4), f[0], f[1], f[2], f[3]);
+            };
+            uint32_t qf[8][4];
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-#pragma unroll
-                for (int r = 0; r < RPT; ++r) {
-                    const int hd = gid + 8 * r;
-                    float2 u = make_float2(0.f, 0.f), w = u;
-                    if (hd < a.g) {
-                        const int64_t off = b * a.q_ts + (j * a.g + hd) * a.q_hs + 16 * ks + 2 * c;
-                        if (a.q_f32) {
-                            const float *qp = static_cast<const float *>(a.q) + off;
-                            u = *reinterpret_cast<const float2 *>(qp);
-                            w = *reinterpret_cast<const float2 *>(qp + 8);
-                        } else {
-                            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + off;
-                            const uint32_t x = *reinterpret_cast<const uint32_t *>(qp);
-                            const uint32_t y = *reinterpret_cast<const uint32_t *>(qp + 8);
-                            u = make_float2(bf16lo(x), bf16hi(x));
-                            w = make_float2(bf16lo(y), bf16hi(y));
-                        }
-                    }
-                    const uint32_t h0 = pack_bf16x2(u.x, u.y), h2 = pack_bf16x2(w.x, w.y);
-                    const uint32_t l0 = pack_bf16x2(u.x - bf16lo(h0), u.y - bf16hi(h0));
-                    const uint32_t l2 = pack_bf16x2(w.x - bf16lo(h2), w.y - bf16hi(h2));
-                    if (RPT == 1) {
-                        qf[ks][0] = h0;
-                        qf[ks][1] = l0;
-                        qf[ks][2] = h2;
-                        qf[ks][3] = l2;
-                    } else {
-                        qf[ks][r] = h0;
-                        qf[ks][2 + r] = h2;
-                        ql[RPT == 2 ? ks : 0][r] = l0;
-                        ql[RPT == 2 ? ks : 0][2 + r] = l2;
-                    }
-                }
-            }
+            for (int ks = 0; ks < 8; ++ks) q_frag(0, ks, qf[ks]);
             float o[16][4];
 #pragma unroll
             for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
@@ -320,29 +328,25 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             for (int e = 0; e < seg_n; ++e, ++i) {
                 if (i % kAmGroups != grp) continue;
                 const int s = i % NS;
-                if (!dead)
-                    dead = !__all_sync(0xffffffffu, !s_flag[0] && mbar_wait(&full[s], (unsigned)(i / NS) & 1u));
-                if (dead) {
-                    s_flag[0] = 1;
-                    continue;
-                }
+                if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&full[s], (unsigned)(i / NS) & 1u));
                 const int kb = sp.block(first + e) * kPdKeys + 16 * wl;  // this warp's 16 keys
-                if (kb < sp.len && (kb + 16 > sp.lo || kb < sp.sk)) {
-                    const unsigned char *st = sm + s * kPdStage;
+                if (!dead && kb < sp.len && (kb + 16 > sp.lo || kb < sp.sk)) {
+                    const unsigned char *st = sm + s * kPdStage + part_off;
                     float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
                     {
-                        const int row = 16 * wl + (lane & 7) + ((lane >> 4) << 3);
+                        const int row = row_in + (lane & 7) + ((lane >> 4) << 3);
                         const int half = (lane >> 3) & 1;
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks) {
                             uint32_t b0_, b1_, b2_, b3_;
-                            ldsm_x4(st + (ks >> 2) * kPdBox + am_swz(row, 2 * (ks & 3) + half), b0_, b1_, b2_, b3_);
+                            ldsm_x4(st + (ks >> 2) * half_bytes + am_swz(row, 2 * (ks & 3) + half), b0_, b1_, b2_, b3_);
                             mma_bf16_16816(s0, qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b0_, b1_);
                             mma_bf16_16816(s1, qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b2_, b3_);
                             if (RPT == 2) {
-                                const int kq = RPT == 2 ? ks : 0;
-                                mma_bf16_16816(s0, ql[kq][0], ql[kq][1], ql[kq][2], ql[kq][3], b0_, b1_);
-                                mma_bf16_16816(s1, ql[kq][0], ql[kq][1], ql[kq][2], ql[kq][3], b2_, b3_);
+                                uint32_t ql[4];
+                                q_frag(1, ks, ql);
+                                mma_bf16_16816(s0, ql[0], ql[1], ql[2], ql[3], b0_, b1_);
+                                mma_bf16_16816(s1, ql[0], ql[1], ql[2], ql[3], b2_, b3_);
                             }
                         }
                     }
@@ -398,12 +402,13 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                         pl[r][1] = pack_bf16x2(p2 - bf16lo(ph[r][1]), p3 - bf16hi(ph[r][1]));
                     }
                     {
-                        const int row = 16 * wl + (lane & 7) + (((lane >> 3) & 1) << 3);
+                        const int row = row_in + (lane & 7) + (((lane >> 3) & 1) << 3);
                         const int half = lane >> 4;
 #pragma unroll
                         for (int n2 = 0; n2 < 8; ++n2) {
                             uint32_t w0, w1, w2, w3;
-                            ldsm_x4_t(st + (2 + (n2 >> 2)) * kPdBox + am_swz(row, 2 * (n2 & 3) + half), w0, w1, w2, w3);
+                            ldsm_x4_t(st + 2 * kPdBox + (n2 >> 2) * half_bytes + am_swz(row, 2 * (n2 & 3) + half), w0, w1, w2,
+                                      w3);
                             w0 &= keep_a;
                             w1 &= keep_b;
                             w2 &= keep_a;
@@ -424,162 +429,211 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
             }
-            if (RPT == 1) {  // rows gid + 8 held the P_lo . V half of the same head
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    o[t][0] += o[t][2];
-                    o[t][1] += o[t][3];
-                }
-            }
+            // ---- leave the state to the merging warps ----
 #pragma unroll
             for (int r = 0; r < RPT; ++r) {
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             }
-            // ---- group 1 hands its state to group 0 (warp wl to warp wl, same
-            //      lanes), whose warps then lay theirs out for the merge ----
-            auto put = [&]() {
+            const int slot = seg % NB;
+            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&st_empty[slot], ((unsigned)(seg / NB) & 1u) ^ 1u));
 #pragma unroll
-                for (int r = 0; r < RPT; ++r) {
-                    const int hd = gid + 8 * r;
-                    if (hd < a.g) {
+            for (int r = 0; r < RPT; ++r) {
+                const int hd = gid + 8 * r;
+                if (hd < a.g) {
+                    float *p = s_o + slot * (SM::STATE / 4) + (warp * GM + hd) * kPdRow + 2 * c;
 #pragma unroll
-                        for (int t = 0; t < 16; ++t)
-                            *reinterpret_cast<float2 *>(&s_o[(wl * GM + hd) * D + 8 * t + 2 * c]) =
-                                make_float2(o[t][2 * r], o[t][2 * r + 1]);
-                        if (c == 0) {
-                            s_ml[(wl * GM + hd) * 2 + 0] = m[r];
-                            s_ml[(wl * GM + hd) * 2 + 1] = l[r];
-                        }
+                    for (int t = 0; t < 16; ++t)  // (GM == 8: rows gid + 8 held the P_lo . V part of the same head)
+                        *reinterpret_cast<float2 *>(p + 8 * t) =
+                            RPT == 1 ? make_float2(o[t][0] + o[t][2], o[t][1] + o[t][3])
+                                     : make_float2(o[t][2 * r], o[t][2 * r + 1]);
+                    if (c == 0)
+                        *reinterpret_cast<float2 *>(s_ml + slot * (SM::ML / 4) + (warp * GM + hd) * 2) = make_float2(m[r], l[r]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st_full[slot]);
+            pair_start = pair_end;
+            if (i < n) w.next(a, s_start);
+        }
+        if (dead) s_flag[0] = 1;
+    } else {
+        // ---- merging warps: thread = two dimensions ----
+        const int tid = threadIdx.x - kPdMergeWarp * 32;
+        auto meet = [] { asm volatile("bar.sync 2, %0;" ::"n"(kPdMergeWarps * 32) : "memory"); };
+        bool dead = false;
+        PdWalk w, ahead;
+        w.open(a, seq_of(u0));
+        int64_t pair_start = s_start[w.b];
+        {
+            const int64_t rel = u0 - pair_start;
+            w.j = (int)(rel / w.sp.nblk);
+            pair_start += (int64_t)w.j * w.sp.nblk;
+        }
+        // the queries of segment seg: rows of hi parts, then of lo parts
+        ahead = w;
+        int64_t ahead_at = pair_start;  // where its pair begins; at or behind u1: no such segment
+        int staged = 0;
+        auto stage_q = [&]() {
+            if (ahead_at >= u1) return;
+            unsigned char *q = s_q + (staged & 1) * SM::Q;
+#pragma unroll
+            for (int r = 0; r < 2 * RPT; ++r) {
+                const int hd = tid / 16 + 4 * r, ch = tid % 16;  // 8 dims
+                float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (hd < a.g) {
+                    const int64_t off = ahead.b * a.q_ts + (ahead.j * a.g + hd) * a.q_hs + 8 * ch;
+                    if (a.q_f32) {
+                        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + off);
+                        const float4 x = p[0], y = p[1];
+                        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + off);
+                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[2 * e] = bf16lo(y[e]), f[2 * e + 1] = bf16hi(y[e]);
                     }
+                }
+                uint32_t h[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+                    lo[e] = pack_bf16x2(f[2 * e] - bf16lo(h[e]), f[2 * e + 1] - bf16hi(h[e]));
+                }
+                const int at = (ch ^ (hd & 7)) << 4;
+                *reinterpret_cast<uint4 *>(q + hd * 256 + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(q + (GM + hd) * 256 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[staged & 1]);
+            ++staged;
+            ahead_at += ahead.sp.nblk;
+            if (ahead_at < u1) ahead.next(a, s_start);
+        };
+        stage_q();
+        stage_q();
+        for (int seg = 0; pair_start < u1; ++seg) {
+            const int64_t pair_end = pair_start + w.sp.nblk;
+            const int slot = seg % NB;
+            const float *so = s_o + slot * (SM::STATE / 4), *sml = s_ml + slot * (SM::ML / 4);
+            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&st_full[slot], (unsigned)(seg / NB) & 1u));
+            if (tid < a.g) {
+                float M = -INFINITY, den = 0.f;
+#pragma unroll
+                for (int x = 0; x < kAmWarps; ++x) M = fmaxf(M, sml[(x * GM + tid) * 2]);
+#pragma unroll
+                for (int x = 0; x < kAmWarps; ++x) {
+                    const float2 ml = *reinterpret_cast<const float2 *>(sml + (x * GM + tid) * 2);
+                    const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                    s_wt[x * GM + tid] = wt;
+                    den += wt * ml.y;
+                }
+                s_M[tid] = M;
+                s_den[tid] = den;
+            }
+            meet();
+            const bool whole = pair_start >= u0 && pair_end <= u1;
+            const int cf = whole ? cta : am_cta_of(U, G, pair_start);
+            auto emit = [&](int hrow, float2 num, float M, float den) {
+                const int64_t row = (int64_t)w.b * a.nq + w.j * a.g + hrow;
+                if (a.own_o) {
+                    *reinterpret_cast<float2 *>(a.own_o + row * D + 2 * tid) = num;
+                    if (tid == 0) {
+                        a.own_ml[row * 2] = M;
+                        a.own_ml[row * 2 + 1] = den;
+                    }
+                } else {
+                    const int64_t at = row * D + 2 * tid;
+                    if (a.o_f32)
+                        *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at) = make_float2(num.x / den, num.y / den);
+                    else
+                        *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at) =
+                            pack_bf16x2(num.x / den, num.y / den);
+                    if (a.lse && tid == 0) a.lse[row] = (M + log2f(den)) * 0.6931471805599453f;
                 }
             };
-            if (grp == 1) put();
-            asm volatile("bar.sync 1, %0;" ::"n"(kAmWarps * 32) : "memory");
-            if (grp == 0) {
+            const int part = 2 * cta + (pair_start > u0 ? 1 : 0);
+            for (int hrow = 0; hrow < a.g; ++hrow) {
+                float2 num = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int r = 0; r < RPT; ++r) {
-                    const int hd = gid + 8 * r;
-                    if (hd < a.g) {
-                        const float m1 = s_ml[(wl * GM + hd) * 2 + 0], l1 = s_ml[(wl * GM + hd) * 2 + 1];
-                        const float M = fmaxf(m[r], m1);
-                        const float w0 = m[r] == -INFINITY ? 0.f : exp2f(m[r] - M);
-                        const float w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
-#pragma unroll
-                        for (int t = 0; t < 16; ++t) {
-                            const float2 x = *reinterpret_cast<const float2 *>(&s_o[(wl * GM + hd) * D + 8 * t + 2 * c]);
-                            o[t][2 * r] = o[t][2 * r] * w0 + x.x * w1;
-                            o[t][2 * r + 1] = o[t][2 * r + 1] * w0 + x.y * w1;
-                        }
-                        l[r] = l[r] * w0 + l1 * w1;
-                        m[r] = M;
-                    }
+                for (int x = 0; x < kAmWarps; ++x) {
+                    const float wt = s_wt[x * GM + hrow];
+                    const float2 y = *reinterpret_cast<const float2 *>(so + (x * GM + hrow) * kPdRow + 2 * tid);
+                    num.x += wt * y.x;
+                    num.y += wt * y.y;
                 }
-                __syncwarp();  // a warp reads and writes only its own part
-                put();
-                asm volatile("bar.sync 2, %0;" ::"n"(kAmGroupWarps * 32) : "memory");
-
-                // ---- group 0 merges its warps; thread = dimension ----
-                const bool whole = pair_start >= u0 && pair_end <= u1;
-                const int cf = whole ? cta : am_cta_of(U, G, pair_start);
-                auto emit = [&](int hrow, float num, float M, float den) {
-                    const int64_t row = (int64_t)b * a.nq + j * a.g + hrow;
-                    if (a.own_o) {
-                        a.own_o[row * D + tid] = num;
-                        if (tid == 0) {
-                            a.own_ml[row * 2] = M;
-                            a.own_ml[row * 2 + 1] = den;
-                        }
-                    } else {
-                        store_act(a.o, a.o_f32, row * D + tid, num / den);
-                        if (a.lse && tid == 0) a.lse[row] = (M + log2f(den)) * 0.6931471805599453f;
-                    }
-                };
-                const int slot = 2 * cta + (pair_start > u0 ? 1 : 0);
-                for (int hrow = 0; hrow < a.g; ++hrow) {
-                    float M = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kAmGroupWarps; ++w) M = fmaxf(M, s_ml[(w * GM + hrow) * 2]);
-                    float num = 0.f, den = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kAmGroupWarps; ++w) {
-                        const float mi = s_ml[(w * GM + hrow) * 2];
-                        const float wt = mi == -INFINITY ? 0.f : exp2f(mi - M);
-                        num += wt * s_o[(w * GM + hrow) * D + tid];
-                        den += wt * s_ml[(w * GM + hrow) * 2 + 1];
-                    }
-                    if (whole) {
-                        emit(hrow, num, M, den);
-                    } else {
-                        a.part_o[((int64_t)slot * a.g + hrow) * D + tid] = num;
-                        if (tid == 0) {
-                            a.part_ml[((int64_t)slot * a.g + hrow) * 2 + 0] = M;
-                            a.part_ml[((int64_t)slot * a.g + hrow) * 2 + 1] = den;
-                        }
-                    }
-                }
-                if (!whole) {
-                    const int n_p = am_cta_of(U, G, pair_end - 1) - cf + 1;
-                    __threadfence();
-                    asm volatile("bar.sync 2, %0;" ::"n"(kAmGroupWarps * 32) : "memory");
+                if (whole) {
+                    emit(hrow, num, s_M[hrow], s_den[hrow]);
+                } else {
+                    *reinterpret_cast<float2 *>(a.part_o + ((int64_t)part * a.g + hrow) * D + 2 * tid) = num;
                     if (tid == 0) {
-                        const unsigned prev = atomicAdd(&a.tickets[cf], 1u);
-                        s_flag[1] = prev == (unsigned)(n_p - 1);
-                        if (prev >= (unsigned)n_p) record_error(2u);
-                    }
-                    asm volatile("bar.sync 2, %0;" ::"n"(kAmGroupWarps * 32) : "memory");
-                    if (s_flag[1]) {
-                        // ---- the last CTA of the pair: partials in CTA order ----
-                        __threadfence();
-                        float *s_mlp = s_o;                          // [n_p][g][2]
-                        float *s_w = s_o + 2 * GM * kPagedMaxCtas;   // [n_p][GM]
-                        float *s_M = s_misc, *s_den = s_misc + GM;
-                        // CTA cf's part of the pair is its second segment when its range begins before the pair
-                        const int slot0 = 2 * cf + (am_start(U, G, cf) < pair_start ? 1 : 0);
-                        auto slot_of = [&](int x) { return x == 0 ? slot0 : 2 * (cf + x); };
-                        for (int x = tid; x < n_p * a.g; x += kAmGroupWarps * 32) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) +
-                                                     (int64_t)slot_of(x / a.g) * a.g + x % a.g);
-                            s_mlp[2 * x] = ml.x;
-                            s_mlp[2 * x + 1] = ml.y;
-                        }
-                        asm volatile("bar.sync 2, %0;" ::"n"(kAmGroupWarps * 32) : "memory");
-                        if (tid < a.g) {
-                            float M = -INFINITY;
-                            for (int x = 0; x < n_p; ++x) M = fmaxf(M, s_mlp[(x * a.g + tid) * 2]);
-                            float den = 0.f;
-                            for (int x = 0; x < n_p; ++x) {
-                                const float mi = s_mlp[(x * a.g + tid) * 2];
-                                const float wt = mi == -INFINITY ? 0.f : exp2f(mi - M);
-                                s_w[x * GM + tid] = wt;
-                                den += wt * s_mlp[(x * a.g + tid) * 2 + 1];
-                            }
-                            s_M[tid] = M;
-                            s_den[tid] = den;
-                        }
-                        asm volatile("bar.sync 2, %0;" ::"n"(kAmGroupWarps * 32) : "memory");
-                        for (int hrow = 0; hrow < a.g; ++hrow) {
-                            float num = 0.f;
-#pragma unroll 8
-                            for (int x = 0; x < n_p; ++x)
-                                num += s_w[x * GM + hrow] *
-                                       __ldcg(a.part_o + ((int64_t)slot_of(x) * a.g + hrow) * D + tid);
-                            emit(hrow, num, s_M[hrow], s_den[hrow]);
-                        }
-                        if (tid == 0) atomicExch(&a.tickets[cf], 0u);
+                        a.part_ml[((int64_t)part * a.g + hrow) * 2 + 0] = s_M[hrow];
+                        a.part_ml[((int64_t)part * a.g + hrow) * 2 + 1] = s_den[hrow];
                     }
                 }
             }
-            // the merge area is rewritten by the next segment
-            asm volatile("bar.sync 1, %0;" ::"n"(kAmWarps * 32) : "memory");
-            pair_start = pair_end;
-            if (i < n && ++j == v.nkv) {
-                j = 0;
-                do ++b;
-                while (s_start[b + 1] == s_start[b]);
-                sp = pd_span(a, paged_len(v, b));
+            if (!whole) {
+                const int n_p = am_cta_of(U, G, pair_end - 1) - cf + 1;
+                __threadfence();
+                meet();
+                if (tid == 0) {
+                    const unsigned prev = atomicAdd(&a.tickets[cf], 1u);
+                    s_flag[1] = prev == (unsigned)(n_p - 1);
+                    if (prev >= (unsigned)n_p) record_error(2u);
+                }
+                meet();
+                if (s_flag[1]) {
+                    // ---- the last CTA of the pair: partials in CTA order.  The state of this
+                    //      segment has been read, so its slot holds the tables. ----
+                    __threadfence();
+                    float *s_mlp = s_o + slot * (SM::STATE / 4);  // [n_p][g][2]
+                    float *s_w = s_mlp + 2 * GM * kPagedMaxCtas;  // [n_p][GM]
+                    // CTA cf's part of the pair is its second segment when its range begins before the pair
+                    const int part0 = 2 * cf + (am_start(U, G, cf) < pair_start ? 1 : 0);
+                    auto part_of = [&](int x) { return x == 0 ? part0 : 2 * (cf + x); };
+                    for (int x = tid; x < n_p * a.g; x += kPdMergeWarps * 32) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) +
+                                                 (int64_t)part_of(x / a.g) * a.g + x % a.g);
+                        s_mlp[2 * x] = ml.x;
+                        s_mlp[2 * x + 1] = ml.y;
+                    }
+                    meet();
+                    if (tid < a.g) {
+                        float M = -INFINITY;
+                        for (int x = 0; x < n_p; ++x) M = fmaxf(M, s_mlp[(x * a.g + tid) * 2]);
+                        float den = 0.f;
+                        for (int x = 0; x < n_p; ++x) {
+                            const float mi = s_mlp[(x * a.g + tid) * 2];
+                            const float wt = mi == -INFINITY ? 0.f : exp2f(mi - M);
+                            s_w[x * GM + tid] = wt;
+                            den += wt * s_mlp[(x * a.g + tid) * 2 + 1];
+                        }
+                        s_M[tid] = M;
+                        s_den[tid] = den;
+                    }
+                    meet();
+                    for (int hrow = 0; hrow < a.g; ++hrow) {
+                        float2 num = make_float2(0.f, 0.f);
+#pragma unroll 8
+                        for (int x = 0; x < n_p; ++x) {
+                            const float wt = s_w[x * GM + hrow];
+                            const float2 y = __ldcg(
+                                reinterpret_cast<const float2 *>(a.part_o + ((int64_t)part_of(x) * a.g + hrow) * D) + tid);
+                            num.x += wt * y.x;
+                            num.y += wt * y.y;
+                        }
+                        emit(hrow, num, s_M[hrow], s_den[hrow]);
+                    }
+                    if (tid == 0) atomicExch(&a.tickets[cf], 0u);
+                }
             }
+            meet();  // everyone has read the weights and the state
+            if (lane == 0) mbar_arrive(&st_empty[slot]);
+            stage_q();  // (its buffer was the finished segment's)
+            pair_start = pair_end;
+            if (pair_start < u1) w.next(a, s_start);
         }
+        if (dead) s_flag[0] = 1;
     }
     __syncthreads();
     if (s_flag[0] && threadIdx.x == 0) {

@@ -127,12 +127,17 @@ int paged_call(const tpl_plan *p, const tpl_paged_kv *kv, const PagedView &v, co
     return TPL_OK;
 }
 
-// The pool as rows of 128 values; boxes of 64 dims x the rows of a page (at most box_max).
-int paged_maps(const PagedCall &c, CUtensorMap *k, CUtensorMap *v, int box_max) {
+// The pool as rows of 128 values: boxes of 64 dims x the rows of a page (at
+// most box_max), or of both halves of the dims one behind the other.
+int paged_maps(const PagedCall &c, CUtensorMap *k, CUtensorMap *v, int box_max, bool halves) {
     const uint64_t rows = (uint64_t)c.v.nkv * c.v.n_pages << c.v.page_shift;
     const uint32_t box = (uint32_t)std::min(1 << c.v.page_shift, box_max);
-    int rc = make_map(k, c.kv->k, 128, rows, 256, 64, box);
-    return rc != TPL_OK ? rc : make_map(v, c.kv->v, 128, rows, 256, 64, box);
+    for (CUtensorMap *m : {k, v}) {
+        const void *pool = m == k ? c.kv->k : c.kv->v;
+        const int rc = halves ? make_map(m, pool, 64, rows, 256, 64, box, 2, 128, 2) : make_map(m, pool, 128, rows, 256, 64, box);
+        if (rc != TPL_OK) return rc;
+    }
+    return TPL_OK;
 }
 
 float paged_scale_log2(const tpl_plan *p) { return 1.4426950408889634f / sqrtf((float)p->d.head_dim); }
@@ -159,7 +164,7 @@ int paged_decode(const PagedCall &c, int window, int sinks, int base, bool own) 
     if (sms <= 0) return TPL_ECUDA;
     PagedDecodeArgs a;
     std::memset(&a, 0, sizeof(a));
-    int rc = paged_maps(c, &a.tm_k, &a.tm_v, kPdKeys);
+    int rc = paged_maps(c, &a.tm_k, &a.tm_v, kPdKeys, true);
     if (rc != TPL_OK) return rc;
     a.v = c.v;
     a.q = c.q->data;
@@ -206,7 +211,7 @@ int paged_prompt_args(const PagedCall &c, PagedPromptArgs *a, int *grid) {
     if (sms <= 0) return TPL_ECUDA;
     *grid = std::min(sms, kPagedMaxCtas);
     std::memset(a, 0, sizeof(*a));
-    int rc = paged_maps(c, &a->tm_k, &a->tm_v, kPtKeys);
+    int rc = paged_maps(c, &a->tm_k, &a->tm_v, kPtKeys, false);
     if (rc != TPL_OK) return rc;
     a->v = c.v;
     a->q = c.q->data;
