@@ -261,8 +261,8 @@ int paged_shared(const PagedCall &c, int shared) {
     s.own_o = reinterpret_cast<const float *>(c.ws + c.L.own_o);
     s.own_ml = reinterpret_cast<const float *>(c.ws + c.L.own_ml);
     const int64_t rows = (int64_t)c.v.n_tokens * a.nq;
-    const int per = kPtJoinThreads / 32;
-    return cuda_rc(launch_pdl(paged_shared_join_kernel, (unsigned)((rows + per - 1) / per), kPtJoinThreads, 0, c.st, s));
+    return cuda_rc(launch_pdl(paged_shared_join_kernel, (unsigned)((rows + kPtJoinRows - 1) / kPtJoinRows), kPtJoinThreads,
+                              0, c.st, s));
 }
 
 }  // namespace

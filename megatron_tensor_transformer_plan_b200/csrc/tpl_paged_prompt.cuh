@@ -785,13 +785,47 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     }
 }
 
-// Joins the partials of the items that were cut: block (c, part) takes 32 rows
-// of the item whose first CTA is c; a warp per row, four dimensions per lane.
-constexpr int kPtJoinRows = 32;
-constexpr int kPtJoinThreads = 256;
+// ---- joins: a warp per row, four dimensions per lane.  A handful of loads
+// ---- each, so latency is what they cost: the parts' maxima and sums are read
+// ---- by a lane each, the outputs several at a time.
 
-__device__ __forceinline__ void paged_store_row(const float4 &num, float M, float den, int lane, int64_t row,
-                                                __nv_bfloat16 *o, float *lse) {
+constexpr int kPtJoinThreads = 256;
+constexpr int kPtJoinRows = kPtJoinThreads / 32;  // rows per block
+
+// The sum over parts x < n of a row: part(x) is its place in part_ml / part_o;
+// extra: one more (max, sum, outputs), or NULL.
+template <typename Part>
+__device__ __forceinline__ void paged_join_row(int lane, int n, const float *part_ml, const float *part_o, Part part,
+                                               const float2 *extra_ml, const float4 *extra_o, int64_t row,
+                                               __nv_bfloat16 *o, float *lse) {
+    auto ml_of = [&](int x) { return __ldcg(reinterpret_cast<const float2 *>(part_ml) + part(x)); };
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 first = lane < n ? ml_of(lane) : none, ext = extra_ml ? __ldcg(extra_ml) : none;
+    float M = fmaxf(first.x, ext.x);
+    for (int x = lane + 32; x < n; x += 32) M = fmaxf(M, ml_of(x).x);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+    auto add = [&](float wt, float l, const float4 *p) {
+        if (wt == 0.f) return;  // nothing seen: the part's outputs may be anything
+        const float4 y = __ldcg(p + lane);
+        num.x += wt * y.x;
+        num.y += wt * y.y;
+        num.z += wt * y.z;
+        num.w += wt * y.w;
+        den += wt * l;
+    };
+    auto weight = [&](float m) { return m == -INFINITY ? 0.f : exp2f(m - M); };
+    for (int x0 = 0; x0 < n; x0 += 32) {
+        const float2 ml = x0 == 0 ? first : x0 + lane < n ? ml_of(x0 + lane) : none;
+        const float wt = weight(ml.x);
+#pragma unroll 4
+        for (int x = 0; x < min(32, n - x0); ++x)
+            add(__shfl_sync(0xffffffffu, wt, x), __shfl_sync(0xffffffffu, ml.y, x),
+                reinterpret_cast<const float4 *>(part_o) + part(x0 + x) * 32);
+    }
+    if (extra_ml) add(weight(ext.x), ext.y, extra_o);
     const float inv = 1.f / den;
     uint2 u = make_uint2(0u, 0u);
     if (den != 0.f) u = make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
@@ -799,17 +833,7 @@ __device__ __forceinline__ void paged_store_row(const float4 &num, float M, floa
     if (lse && lane == 0) lse[row] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
 }
 
-__device__ __forceinline__ void paged_add_part(float4 &num, float &den, float M, float m, float l, const float4 *part) {
-    if (m == -INFINITY) return;  // nothing seen: the part's outputs may be anything
-    const float wt = exp2f(m - M);
-    const float4 x = __ldcg(part);
-    num.x += wt * x.x;
-    num.y += wt * x.y;
-    num.z += wt * x.z;
-    num.w += wt * x.w;
-    den += wt * l;
-}
-
+// The items that were cut: block (c, k) takes rows kPtJoinRows k .. of the item whose first CTA is c.
 __global__ void __launch_bounds__(kPtJoinThreads) paged_prompt_join_kernel(const __grid_constant__ PagedPromptArgs a) {
     pdl_wait();
     pdl_trigger();
@@ -817,25 +841,17 @@ __global__ void __launch_bounds__(kPtJoinThreads) paged_prompt_join_kernel(const
     const int4 cut = a.cut[c];
     if (cut.w == 0) return;
     const int ntok = cut.y & 0xffff, slot0 = 2 * c + (cut.y >> 30 & 1);
-    for (int k = warp; k < kPtJoinRows; k += kPtJoinThreads / 32) {
-        const int rr = blockIdx.y * kPtJoinRows + k, r = rr & 127;
-        const int tok = (rr >> 7) * a.tb + r / a.g;
-        if (r >= a.tb * a.g || tok >= ntok) continue;
-        const int64_t row = (int64_t)(cut.x + tok) * a.nq + cut.z * a.g + r % a.g;
-        auto part = [&](int x) { return (int64_t)(x == 0 ? slot0 : 2 * (c + x)) * a.part_rows + rr; };
-        float M = -INFINITY, den = 0.f;
-        for (int x = 0; x < cut.w; ++x) M = fmaxf(M, __ldcg(a.part_ml + part(x) * 2));
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = 0; x < cut.w; ++x) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + part(x));
-            paged_add_part(num, den, M, ml.x, ml.y, reinterpret_cast<const float4 *>(a.part_o) + part(x) * 32 + lane);
-        }
-        paged_store_row(num, M, den, lane, row, a.o, a.lse);
-    }
+    const int rr = blockIdx.y * kPtJoinRows + warp, r = rr & 127;
+    const int tok = (rr >> 7) * a.tb + r / a.g;
+    if (r >= a.tb * a.g || tok >= ntok) return;
+    const int64_t row = (int64_t)(cut.x + tok) * a.nq + cut.z * a.g + r % a.g;
+    paged_join_row(lane, cut.w, a.part_ml, a.part_o,
+                   [&](int x) { return (int64_t)(x == 0 ? slot0 : 2 * (c + x)) * a.part_rows + rr; }, nullptr, nullptr, row,
+                   a.o, a.lse);
 }
 
-// Joins, for every (sequence, query head) of a batch behind a common prefix,
-// the prefix's partials and what the sequence's own keys gave.
+// For every (sequence, query head) of a batch behind a common prefix: the
+// prefix's partials and what the sequence's own keys gave.
 struct PagedSharedJoinArgs {
     PagedPromptArgs p;
     int G;                       // CTAs the prefix was cut into
@@ -847,7 +863,7 @@ __global__ void __launch_bounds__(kPtJoinThreads) paged_shared_join_kernel(const
     pdl_trigger();
     const PagedPromptArgs &a = g.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * (kPtJoinThreads / 32) + warp;
+    const int64_t row = (int64_t)blockIdx.x * kPtJoinRows + warp;
     if (row >= (int64_t)a.v.n_tokens * a.nq) return;
     const int b = (int)(row / a.nq), head = (int)(row % a.nq), j = head / a.g;
     const int items = pt_items(a, a.v.n_tokens), it = b / (2 * a.tb), tok = b % (2 * a.tb);
@@ -855,17 +871,9 @@ __global__ void __launch_bounds__(kPtJoinThreads) paged_shared_join_kernel(const
     const int64_t NT = (a.shared + kPtKeys - 1) / kPtKeys, idx = (int64_t)j * items + it;
     const int64_t U = NT * items * a.v.nkv;
     const int cf = am_cta_of(U, g.G, idx * NT), cl = am_cta_of(U, g.G, idx * NT + NT - 1);
-    auto part = [&](int c) { return (idx + c) * a.part_rows + rr; };
-    const float2 own = __ldcg(reinterpret_cast<const float2 *>(g.own_ml) + row);
-    float M = own.x, den = 0.f;
-    for (int c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(a.part_ml + part(c) * 2));
-    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = cf; c <= cl; ++c) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + part(c));
-        paged_add_part(num, den, M, ml.x, ml.y, reinterpret_cast<const float4 *>(a.part_o) + part(c) * 32 + lane);
-    }
-    paged_add_part(num, den, M, own.x, own.y, reinterpret_cast<const float4 *>(g.own_o) + row * 32 + lane);
-    paged_store_row(num, M, den, lane, row, a.o, a.lse);
+    paged_join_row(lane, cl - cf + 1, a.part_ml, a.part_o, [&](int x) { return (idx + cf + x) * a.part_rows + rr; },
+                   reinterpret_cast<const float2 *>(g.own_ml) + row,
+                   reinterpret_cast<const float4 *>(g.own_o) + row * 32, row, a.o, a.lse);
 }
 
 }  // namespace tpl
