@@ -61,6 +61,13 @@ __device__ __forceinline__ int64_t paged_row(const PagedView &v, int b, int entr
     return (((int64_t)sh * v.n_pages + page) * v.nkv_s + jl) << v.page_shift;
 }
 
+// 2^x by the special-function unit (relative error 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---- append ----------------------------------------------------------------
 //
 // q' = R(p) q, and for the token's slot of the cache K = bf16(R(p) k), V =

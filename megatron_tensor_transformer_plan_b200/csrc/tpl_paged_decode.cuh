@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             PdWalk w;
             w.open(a, seq_of(u));
             const int64_t rel = u - s_start[w.b];
-            w.j = (int)(rel / w.sp.nblk);
+            w.j = rel >> 32 ? (int)(rel / w.sp.nblk) : (int)((uint32_t)rel / (uint32_t)w.sp.nblk);
             const int key = w.sp.block((int)(rel - (int64_t)w.j * w.sp.nblk)) * kPdKeys + ((lane % nsub) << box_shift);
             const bool want = i0 + lane / nsub < n && key < w.sp.len && (key + (1 << box_shift) > w.sp.lo || key < w.sp.sk);
             if (!want) return -1;
@@ -334,20 +334,28 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                     const unsigned char *st = sm + s * kPdStage + part_off;
                     float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
                     {
+                        // even and odd steps add up apart: half the chain of dependent products
+                        float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
                         const int row = row_in + (lane & 7) + ((lane >> 4) << 3);
                         const int half = (lane >> 3) & 1;
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks) {
                             uint32_t b0_, b1_, b2_, b3_;
                             ldsm_x4(st + (ks >> 2) * half_bytes + am_swz(row, 2 * (ks & 3) + half), b0_, b1_, b2_, b3_);
-                            mma_bf16_16816(s0, qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b0_, b1_);
-                            mma_bf16_16816(s1, qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b2_, b3_);
+                            float(&y0)[4] = ks & 1 ? t0 : s0, (&y1)[4] = ks & 1 ? t1 : s1;
+                            mma_bf16_16816(y0, qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b0_, b1_);
+                            mma_bf16_16816(y1, qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b2_, b3_);
                             if (RPT == 2) {
                                 uint32_t ql[4];
                                 q_frag(1, ks, ql);
-                                mma_bf16_16816(s0, ql[0], ql[1], ql[2], ql[3], b0_, b1_);
-                                mma_bf16_16816(s1, ql[0], ql[1], ql[2], ql[3], b2_, b3_);
+                                mma_bf16_16816(y0, ql[0], ql[1], ql[2], ql[3], b0_, b1_);
+                                mma_bf16_16816(y1, ql[0], ql[1], ql[2], ql[3], b2_, b3_);
                             }
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            s0[x] += t0[x];
+                            s1[x] += t1[x];
                         }
                     }
                     // this thread's keys: kb + 2c, +1, +8, +9
@@ -393,8 +401,8 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                                 }
                             }
                         }
-                        const float p0 = exp2f(x0 - m[r]), p1 = exp2f(x1 - m[r]), p2 = exp2f(x2 - m[r]),
-                                    p3 = exp2f(x3 - m[r]);
+                        const float p0 = ex2(x0 - m[r]), p1 = ex2(x1 - m[r]), p2 = ex2(x2 - m[r]),
+                                    p3 = ex2(x3 - m[r]);
                         l[r] += (p0 + p1) + (p2 + p3);
                         ph[r][0] = pack_bf16x2(p0, p1);
                         ph[r][1] = pack_bf16x2(p2, p3);
@@ -458,8 +466,8 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         }
         if (dead) s_flag[0] = 1;
     } else {
-        // ---- merging warps: thread = two dimensions ----
-        const int tid = threadIdx.x - kPdMergeWarp * 32;
+        // ---- merging warps: every other head each, a lane four dimensions ----
+        const int tid = threadIdx.x - kPdMergeWarp * 32, mw = warp - kPdMergeWarp;
         auto meet = [] { asm volatile("bar.sync 2, %0;" ::"n"(kPdMergeWarps * 32) : "memory"); };
         bool dead = false;
         PdWalk w, ahead;
@@ -517,6 +525,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             const int slot = seg % NB;
             const float *so = s_o + slot * (SM::STATE / 4), *sml = s_ml + slot * (SM::ML / 4);
             if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&st_full[slot], (unsigned)(seg / NB) & 1u));
+            stage_q();  // (into the buffer of this segment: every consumer is done with it)
             if (tid < a.g) {
                 float M = -INFINITY, den = 0.f;
 #pragma unroll
@@ -534,42 +543,41 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             meet();
             const bool whole = pair_start >= u0 && pair_end <= u1;
             const int cf = whole ? cta : am_cta_of(U, G, pair_start);
-            auto emit = [&](int hrow, float2 num, float M, float den) {
+            auto emit = [&](int hrow, const float4 &num, float M, float den) {
                 const int64_t row = (int64_t)w.b * a.nq + w.j * a.g + hrow;
                 if (a.own_o) {
-                    *reinterpret_cast<float2 *>(a.own_o + row * D + 2 * tid) = num;
-                    if (tid == 0) {
-                        a.own_ml[row * 2] = M;
-                        a.own_ml[row * 2 + 1] = den;
-                    }
+                    reinterpret_cast<float4 *>(a.own_o + row * D)[lane] = num;
+                    if (lane == 0) *reinterpret_cast<float2 *>(a.own_ml + row * 2) = make_float2(M, den);
                 } else {
-                    const int64_t at = row * D + 2 * tid;
+                    const float inv = 1.f / den;
                     if (a.o_f32)
-                        *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at) = make_float2(num.x / den, num.y / den);
+                        reinterpret_cast<float4 *>(static_cast<float *>(a.o) + row * D)[lane] =
+                            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
                     else
-                        *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at) =
-                            pack_bf16x2(num.x / den, num.y / den);
-                    if (a.lse && tid == 0) a.lse[row] = (M + log2f(den)) * 0.6931471805599453f;
+                        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D)[lane] =
+                            make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+                    if (a.lse && lane == 0) a.lse[row] = (M + log2f(den)) * 0.6931471805599453f;
                 }
             };
-            const int part = 2 * cta + (pair_start > u0 ? 1 : 0);
-            for (int hrow = 0; hrow < a.g; ++hrow) {
-                float2 num = make_float2(0.f, 0.f);
+            auto add = [](float4 &num, float wt, const float4 &y) {
+                num.x += wt * y.x;
+                num.y += wt * y.y;
+                num.z += wt * y.z;
+                num.w += wt * y.w;
+            };
+            const int64_t part = 2 * cta + (pair_start > u0 ? 1 : 0);
+#pragma unroll 2
+            for (int hrow = mw; hrow < a.g; hrow += kPdMergeWarps) {
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int x = 0; x < kAmWarps; ++x) {
-                    const float wt = s_wt[x * GM + hrow];
-                    const float2 y = *reinterpret_cast<const float2 *>(so + (x * GM + hrow) * kPdRow + 2 * tid);
-                    num.x += wt * y.x;
-                    num.y += wt * y.y;
-                }
+                for (int x = 0; x < kAmWarps; ++x)
+                    add(num, s_wt[x * GM + hrow], reinterpret_cast<const float4 *>(so + (x * GM + hrow) * kPdRow)[lane]);
                 if (whole) {
                     emit(hrow, num, s_M[hrow], s_den[hrow]);
                 } else {
-                    *reinterpret_cast<float2 *>(a.part_o + ((int64_t)part * a.g + hrow) * D + 2 * tid) = num;
-                    if (tid == 0) {
-                        a.part_ml[((int64_t)part * a.g + hrow) * 2 + 0] = s_M[hrow];
-                        a.part_ml[((int64_t)part * a.g + hrow) * 2 + 1] = s_den[hrow];
-                    }
+                    reinterpret_cast<float4 *>(a.part_o + (part * a.g + hrow) * D)[lane] = num;
+                    if (lane == 0)
+                        *reinterpret_cast<float2 *>(a.part_ml + (part * a.g + hrow) * 2) = make_float2(s_M[hrow], s_den[hrow]);
                 }
             }
             if (!whole) {
@@ -612,16 +620,13 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                         s_den[tid] = den;
                     }
                     meet();
-                    for (int hrow = 0; hrow < a.g; ++hrow) {
-                        float2 num = make_float2(0.f, 0.f);
+#pragma unroll 2
+                    for (int hrow = mw; hrow < a.g; hrow += kPdMergeWarps) {
+                        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-                        for (int x = 0; x < n_p; ++x) {
-                            const float wt = s_w[x * GM + hrow];
-                            const float2 y = __ldcg(
-                                reinterpret_cast<const float2 *>(a.part_o + ((int64_t)part_of(x) * a.g + hrow) * D) + tid);
-                            num.x += wt * y.x;
-                            num.y += wt * y.y;
-                        }
+                        for (int x = 0; x < n_p; ++x)
+                            add(num, s_w[x * GM + hrow],
+                                __ldcg(reinterpret_cast<const float4 *>(a.part_o + ((int64_t)part_of(x) * a.g + hrow) * D) + lane));
                         emit(hrow, num, s_M[hrow], s_den[hrow]);
                     }
                     if (tid == 0) atomicExch(&a.tickets[cf], 0u);
@@ -629,7 +634,6 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             }
             meet();  // everyone has read the weights and the state
             if (lane == 0) mbar_arrive(&st_empty[slot]);
-            stage_q();  // (its buffer was the finished segment's)
             pair_start = pair_end;
             if (pair_start < u1) w.next(a, s_start);
         }

@@ -179,13 +179,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 2^x by the special-function unit (relative error 2^-22; 2^-inf = 0).
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Two fp32 values at a time: the fma and add units take packed pairs.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
