@@ -228,25 +228,39 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
-def _on_current_device(*tensors) -> None:
-    """The library takes plain pointers, so a tensor that is elsewhere is
-    refused here (None: an argument left out)."""
+def _device_and_stream():
+    """The current device and its current stream (a serving loop makes the
+    paged-cache calls one by one, so both are taken the short way)."""
     import torch
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on_device(dev: int, *tensors) -> None:
+    """The library takes plain pointers, so a tensor that is not on the
+    current device is refused here (None: an argument left out)."""
     for x in tensors:
-        if x is None:
-            continue
-        if not x.is_cuda:
-            raise ValueError("a paged-cache tensor is not on a CUDA device")
-        if x.device.index != torch.cuda.current_device():
-            raise ValueError(f"a paged-cache tensor is on {x.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+        if x is not None and x.get_device() != dev:
+            raise ValueError(f"a paged-cache tensor is on {x.device}, the current device is CUDA device {dev}")
+
+
+def _cuda_device(*tensors) -> int:
+    """The CUDA device that all of the tensors are on."""
+    dev = tensors[0].get_device()
+    for x in tensors:
+        if x is not None and (x.get_device() < 0 or x.get_device() != dev):
+            raise ValueError("the paged-cache tensors are not on one CUDA device")
+    return dev
+
+
+_head_types: dict = {}  # torch type -> TPL_BF16, TPL_F32
 
 
 class PagedKV:
     """tpl_paged_kv over two pool tensors, which it keeps alive."""
 
     def __init__(self, k, v):
-        self.k, self.v = k, v
+        self.k, self.v, self.device = k, v, _cuda_device(k, v)
         self.c = tpl_paged_kv(k.data_ptr(), v.data_ptr(), k.shape[1], k.shape[3])
 
 
@@ -255,6 +269,7 @@ class PagedBatch:
 
     def __init__(self, page_table, kv_len, q_start, n_tokens):
         self.page_table, self.kv_len, self.q_start, self.n_tokens = page_table, kv_len, q_start, n_tokens
+        self.device = _cuda_device(page_table, kv_len, q_start)
         n, entries = page_table.shape
         stride = page_table.stride(0) if n > 1 else max(entries, page_table.stride(0))
         self.c = tpl_paged_batch(page_table.data_ptr(), stride, entries, n, kv_len.data_ptr(), _ptr(q_start),
@@ -446,7 +461,6 @@ class Plan:
                                  f"head_dim={d.head_dim}")
         if k.shape != v.shape:
             raise ValueError("paged_kv: k and v differ in shape")
-        _on_current_device(k, v)
         return PagedKV(k, v)
 
     @staticmethod
@@ -467,7 +481,6 @@ class Plan:
             n_tokens = n
         elif q_start.shape != (n + 1,) or n_tokens is None:
             raise ValueError("paged_batch: q_start is [n_seqs + 1] and needs n_tokens")
-        _on_current_device(page_table, kv_len, q_start)
         return PagedBatch(page_table, kv_len, q_start, n_tokens)
 
     def paged_workspace_size(self, n_seqs: int, n_tokens: int) -> int:
@@ -483,67 +496,78 @@ class Plan:
         return ws
 
     @staticmethod
-    def _heads(x, rows: int, heads: int, head_dim: int, name: str):
+    def _heads(x, rows: int, heads: int, head_dim: int, dev: int, name: str):
         """tpl_heads of a tensor [rows][heads][head_dim] with any strides
         between its heads (or [rows][heads * head_dim])."""
-        import torch
         if x is None:
             return None
+        if not _head_types:
+            import torch
+            _head_types.update({torch.bfloat16: TPL_BF16, torch.float32: TPL_F32})
         if x.dim() == 2 and x.shape[1] == heads * head_dim:
             x = x.unflatten(1, (heads, head_dim))
-        if tuple(x.shape) != (rows, heads, head_dim) or (rows > 0 and x.stride(2) != 1):
-            raise ValueError(f"{name}: expected [{rows}][{heads}][{head_dim}] with contiguous heads, got "
-                             f"{tuple(x.shape)}")
-        if x.dtype not in (torch.bfloat16, torch.float32):
+        if x.shape != (rows, heads, head_dim):
+            raise ValueError(f"{name}: expected [{rows}][{heads}][{head_dim}], got {tuple(x.shape)}")
+        ts, hs, es = x.stride()
+        if es != 1 and rows > 0:
+            raise ValueError(f"{name}: the values of a head are not contiguous")
+        kind = _head_types.get(x.dtype)
+        if kind is None:
             raise ValueError(f"{name}: bf16 or fp32, got {x.dtype}")
-        _on_current_device(x)
-        ts, hs, _ = x.stride()
+        _on_device(dev, x)
         # a dimension of one element has no stride of its own
-        ts, hs = (ts if rows > 1 else heads * head_dim), (hs if heads > 1 else head_dim)
-        return ctypes.byref(tpl_heads(x.data_ptr(), TPL_F32 if x.dtype == torch.float32 else TPL_BF16, ts, hs))
+        return tpl_heads(x.data_ptr(), kind, ts if rows > 1 else heads * head_dim, hs if heads > 1 else head_dim)
 
-    def _paged_out(self, batch, o, lse, name):
-        import torch
+    def _paged_out(self, batch, o, lse, dev, name):
         d, n = self.dims, batch.n_tokens
         if o.dtype != self.act_dtype or o.numel() != n * d.n_q_heads * d.head_dim or not o.is_contiguous():
             raise ValueError(f"{name}: o is a contiguous {self.act_dtype} tensor [{n}][{d.n_q_heads * d.head_dim}]")
-        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, d.n_q_heads) or
-                                not lse.is_contiguous()):
-            raise ValueError(f"{name}: lse is a contiguous fp32 tensor [{n}][{d.n_q_heads}]")
-        _on_current_device(o, lse)
+        if lse is not None:
+            import torch
+            if lse.dtype != torch.float32 or lse.shape != (n, d.n_q_heads) or not lse.is_contiguous():
+                raise ValueError(f"{name}: lse is a contiguous fp32 tensor [{n}][{d.n_q_heads}]")
+        _on_device(dev, o, lse)
+
+    @staticmethod
+    def _paged_ready(kv, batch, name):
+        """(device, stream) of a call: the cache and the batch are on the current device."""
+        dev, stream = _device_and_stream()
+        if kv.device != dev or batch.device != dev:
+            raise ValueError(f"{name}: the cache is on CUDA device {kv.device}, the batch on {batch.device}, the current "
+                             f"device is {dev}")
+        return dev, stream
 
     def paged_append(self, kv: PagedKV, batch: PagedBatch, k, v, q=None, q_out=None):
         """Put k, v [n_tokens][n_kv][d] into their slots (turned with TPL_ROPE)
         and q [n_tokens][n_q][d], turned, into q_out (default: in place)."""
         d, n = self.dims, batch.n_tokens
-        if q_out is None:
-            q_out = q
-        _on_current_device(kv.k, kv.v, batch.page_table, batch.kv_len, batch.q_start)
-        check(tpl_paged_append(self.handle, ctypes.byref(kv.c), ctypes.byref(batch.c),
-                               self._heads(q, n, d.n_q_heads, d.head_dim, "paged_append: q"),
-                               self._heads(q_out, n, d.n_q_heads, d.head_dim, "paged_append: q_out"),
-                               self._heads(k, n, d.n_kv_heads, d.head_dim, "paged_append: k"),
-                               self._heads(v, n, d.n_kv_heads, d.head_dim, "paged_append: v"), _stream()),
-              "tpl_paged_append")
+        nq, nkv, hd = d.n_q_heads, d.n_kv_heads, d.head_dim
+        dev, stream = self._paged_ready(kv, batch, "paged_append")
+        qs = self._heads(q, n, nq, hd, dev, "paged_append: q")
+        qo = qs if q_out is None else self._heads(q_out, n, nq, hd, dev, "paged_append: q_out")
+        check(tpl_paged_append(self.handle, kv.c, batch.c, qs, qo, self._heads(k, n, nkv, hd, dev, "paged_append: k"),
+                               self._heads(v, n, nkv, hd, dev, "paged_append: v"), stream), "tpl_paged_append")
 
     def paged_attn(self, kv: PagedKV, batch: PagedBatch, q, o, ws, window: int = 0, sinks: int = 0, lse=None):
         """Attention of the batch's tokens over their pages into o (and lse)."""
         d = self.dims
-        self._paged_out(batch, o, lse, "paged_attn")
-        _on_current_device(kv.k, kv.v, batch.page_table, batch.kv_len, batch.q_start, ws)
-        check(tpl_paged_attn(self.handle, ctypes.byref(kv.c), ctypes.byref(batch.c),
-                             self._heads(q, batch.n_tokens, d.n_q_heads, d.head_dim, "paged_attn: q"), window, sinks,
-                             o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream()), "tpl_paged_attn")
+        dev, stream = self._paged_ready(kv, batch, "paged_attn")
+        self._paged_out(batch, o, lse, dev, "paged_attn")
+        _on_device(dev, ws)
+        check(tpl_paged_attn(self.handle, kv.c, batch.c,
+                             self._heads(q, batch.n_tokens, d.n_q_heads, d.head_dim, dev, "paged_attn: q"), window, sinks,
+                             o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), stream), "tpl_paged_attn")
 
     def paged_attn_shared(self, kv: PagedKV, batch: PagedBatch, shared_len: int, q, o, ws, lse=None):
         """paged_attn of a decode batch whose sequences all begin with the same
         shared_len keys (the same first pages), which are read once."""
         d = self.dims
-        self._paged_out(batch, o, lse, "paged_attn_shared")
-        _on_current_device(kv.k, kv.v, batch.page_table, batch.kv_len, batch.q_start, ws)
-        check(tpl_paged_attn_shared(self.handle, ctypes.byref(kv.c), ctypes.byref(batch.c), shared_len,
-                                    self._heads(q, batch.n_tokens, d.n_q_heads, d.head_dim, "paged_attn_shared: q"),
-                                    o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream()),
+        dev, stream = self._paged_ready(kv, batch, "paged_attn_shared")
+        self._paged_out(batch, o, lse, dev, "paged_attn_shared")
+        _on_device(dev, ws)
+        check(tpl_paged_attn_shared(self.handle, kv.c, batch.c, shared_len,
+                                    self._heads(q, batch.n_tokens, d.n_q_heads, d.head_dim, dev, "paged_attn_shared: q"),
+                                    o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), stream),
               "tpl_paged_attn_shared")
 
     def last_device_error(self) -> int:
