@@ -62,8 +62,8 @@ struct PdSmem {
     static constexpr int Q = 2 * GM * 256;                     // hi rows, lo rows; two pairs
     static constexpr int JOIN = kAmWarps * GM * 4 + 2 * GM * 4;  // the merge's weights, maxima and sums
     static constexpr int BAR = 512;
-    static constexpr int SCAN = (kPagedMaxSeqs + 1) * 8;
-    static constexpr size_t BYTES = (size_t)NS * kPdStage + 2 * Q + SLOTS * (STATE + ML) + JOIN + BAR + SCAN + 1024;
+    static constexpr int SCAN = (kPagedMaxSeqs + 1) * 8 + kPagedMaxSeqs * 4;
+    static constexpr size_t BYTES = (size_t)NS * kPdStage + 2 * Q + SLOTS * (STATE + ML) + JOIN + BAR + SCAN;
     static_assert(BYTES <= 232448, "shared memory per block");
     static_assert(kPagedMaxCtas * GM * 3 * 4 <= STATE, "the join's tables");
 };
@@ -85,7 +85,9 @@ struct PagedDecodeArgs {
     int o_f32;
     float *lse;              // [n_seqs][nq] or NULL
     float *own_o;            // when set (a shared prefix): unnormalised fp32 outputs [n_seqs][nq][128]
-    float *own_ml;           // and (max, sum) [n_seqs][nq][2] instead of o and lse
+    float *own_ml;           // and (max, sum) [n_seqs][nq][2] instead of o and lse.  The kernel before this
+                             // one is then the prefix's: it has waited for all that came before, and nothing
+                             // here needs it, so this one starts at once and waits for it at its end.
 };
 
 // What one sequence's token sees, in keys and in blocks.
@@ -113,17 +115,17 @@ __device__ __forceinline__ PdSpan pd_span(const PagedDecodeArgs &a, int len) {
 struct PdWalk {
     int b, j;
     PdSpan sp;
-    __device__ __forceinline__ void open(const PagedDecodeArgs &a, int b_) {
+    __device__ __forceinline__ void open(const PagedDecodeArgs &a, const int *len, int b_) {
         b = b_;
-        sp = pd_span(a, paged_len(a.v, b));
+        sp = pd_span(a, len[b]);
     }
     // the next pair
-    __device__ __forceinline__ void next(const PagedDecodeArgs &a, const long long *start) {
+    __device__ __forceinline__ void next(const PagedDecodeArgs &a, const long long *start, const int *len) {
         if (++j == a.v.nkv) {
             j = 0;
             do ++b;
             while (start[b + 1] == start[b]);
-            open(a, b);
+            open(a, len, b);
         }
     }
 };
@@ -135,7 +137,11 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     constexpr int NS = SM::NS, NB = SM::SLOTS;
     constexpr int RPT = GM / 8;  // rows (heads) per thread
     extern __shared__ __align__(1024) unsigned char pd_raw[];
-    unsigned char *sm = reinterpret_cast<unsigned char *>(((uintptr_t)pd_raw + 1023) & ~(uintptr_t)1023);
+    unsigned char *sm = pd_raw;
+    if (smem_u32(sm) & 1023u) {  // (the whole grid: the swizzled stages need 1 KB alignment)
+        if (threadIdx.x == 0) record_error(8u);
+        return;
+    }
     unsigned char *s_q = sm + NS * kPdStage;                                   // [2][hi, lo][GM][256 B], swizzled
     float *s_o = reinterpret_cast<float *>(s_q + 2 * SM::Q);                   // [NB][8 warps][GM][kPdRow]
     float *s_ml = s_o + NB * SM::STATE / 4;                                    // [NB][8 warps][GM][2]
@@ -150,6 +156,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     long long *s_warp = reinterpret_cast<long long *>(st_empty + NB + 2);    // [warps]
     static_assert((2 * NS + 2 + 2 * NB + 2 + kPdThreads / 32) * 8 <= SM::BAR, "barrier area");
     long long *s_start = reinterpret_cast<long long *>(reinterpret_cast<unsigned char *>(full) + SM::BAR);  // [n_seqs + 1]
+    int *s_len = reinterpret_cast<int *>(s_start + kPagedMaxSeqs + 1);  // [n_seqs]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         s_flag[2] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    pdl_wait();
+    if (!a.own_o) pdl_wait();
     pdl_trigger();
 
     // ---- prefix sums of the sequences' blocks (all kv heads) ----
@@ -180,7 +187,12 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
 #pragma unroll
         for (int x = 0; x < PT; ++x) {
             const int b = threadIdx.x * per + x;
-            mine[x] = x < per && b < v.n_seqs ? (long long)pd_span(a, paged_len(v, b)).nblk * v.nkv : 0;
+            mine[x] = 0;
+            if (x < per && b < v.n_seqs) {
+                const int len = paged_len(v, b);
+                s_len[b] = len;
+                mine[x] = (long long)pd_span(a, len).nblk * v.nkv;
+            }
             sum += mine[x];
         }
         long long inc = sum;
@@ -221,7 +233,10 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             }
         }
     }
-    if (cta >= G || U == 0) return;  // the whole CTA: nothing in flight
+    if (cta >= G || U == 0) {  // the whole CTA: nothing in flight
+        if (a.own_o) pdl_wait();
+        return;
+    }
 
     const int64_t u0 = am_start(U, G, cta), u1 = am_start(U, G, cta + 1);
     const int n = (int)(u1 - u0);
@@ -248,7 +263,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             const int i = min(i0 + lane / nsub, n - 1);
             const int64_t u = u0 + i;
             PdWalk w;
-            w.open(a, seq_of(u));
+            w.open(a, s_len, seq_of(u));
             const int64_t rel = u - s_start[w.b];
             w.j = rel >> 32 ? (int)(rel / w.sp.nblk) : (int)((uint32_t)rel / (uint32_t)w.sp.nblk);
             const int key = w.sp.block((int)(rel - (int64_t)w.j * w.sp.nblk)) * kPdKeys + ((lane % nsub) << box_shift);
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         const int row_in = (16 * wl) & ((1 << box_shift) - 1);
         const unsigned part_off = (unsigned)((16 * wl) >> box_shift) * 2 * half_bytes;
         PdWalk w;
-        w.open(a, seq_of(u0));
+        w.open(a, s_len, seq_of(u0));
         int64_t pair_start = s_start[w.b];
         {
             const int64_t rel = u0 - pair_start;
@@ -462,7 +477,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(&st_full[slot]);
             pair_start = pair_end;
-            if (i < n) w.next(a, s_start);
+            if (i < n) w.next(a, s_start, s_len);
         }
         if (dead) s_flag[0] = 1;
     } else {
@@ -471,7 +486,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         auto meet = [] { asm volatile("bar.sync 2, %0;" ::"n"(kPdMergeWarps * 32) : "memory"); };
         bool dead = false;
         PdWalk w, ahead;
-        w.open(a, seq_of(u0));
+        w.open(a, s_len, seq_of(u0));
         int64_t pair_start = s_start[w.b];
         {
             const int64_t rel = u0 - pair_start;
@@ -516,7 +531,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             if (lane == 0) mbar_arrive(&q_full[staged & 1]);
             ++staged;
             ahead_at += ahead.sp.nblk;
-            if (ahead_at < u1) ahead.next(a, s_start);
+            if (ahead_at < u1) ahead.next(a, s_start, s_len);
         };
         stage_q();
         stage_q();
@@ -635,7 +650,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             meet();  // everyone has read the weights and the state
             if (lane == 0) mbar_arrive(&st_empty[slot]);
             pair_start = pair_end;
-            if (pair_start < u1) w.next(a, s_start);
+            if (pair_start < u1) w.next(a, s_start, s_len);
         }
         if (dead) s_flag[0] = 1;
     }
@@ -647,6 +662,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         for (int x = issued - NS > 0 ? issued - NS : 0; x < issued; ++x)
             mbar_wait(&full[x % NS], (unsigned)(x / NS) & 1u);
     }
+    if (a.own_o) pdl_wait();
 }
 
 }  // namespace tpl
