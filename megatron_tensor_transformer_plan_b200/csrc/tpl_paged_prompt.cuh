@@ -236,8 +236,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     }
     unsigned char *s_q = sm;              // [tile][part][half][128 rows][128 B]
     unsigned char *ring = sm + SM::Q;
-    uint64_t *full = reinterpret_cast<uint64_t *>(ring + NST * kPtTile);  // [NST] tile landed
-    uint64_t *empty = full + NST;         // [NST] tile read by its last MMA
+    // A stage holds a K and a V tile in turn (NST is odd).  Each kind has its own barriers
+    // for having landed, with a phase per two laps: a wait names a phase by its parity, so
+    // whoever waits for one kind must not depend on having seen the other.
+    uint64_t *full_k = reinterpret_cast<uint64_t *>(ring + NST * kPtTile);  // [NST]
+    uint64_t *full_v = full_k + NST;      // [NST]
+    uint64_t *empty = full_v + NST;       // [NST] tile read by its last MMA
     uint64_t *v_ready = empty + NST;      // [NST] V tile checked
     uint64_t *q_ready = v_ready + NST;    // [2]
     uint64_t *s_full = q_ready + 2;       // [2 tiles][2 halves]
@@ -251,13 +255,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     int *s_issued = const_cast<int *>(s_fail) + 1;
     int *s_where = s_issued + 1;          // [4] start of this CTA's range: j, b, item, tiles before
     long long *s_sum = reinterpret_cast<long long *>((reinterpret_cast<uintptr_t>(s_where + 4) + 7) & ~(uintptr_t)7);
-    static_assert((3 * NST + 17) * 8 + 40 + 16 + kPtThreads / 32 * 8 <= SM::BAR, "barrier area");
+    static_assert((4 * NST + 17) * 8 + 40 + 16 + kPtThreads / 32 * 8 <= SM::BAR, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full_k[s], 1);
+            mbar_init(&full_v[s], 1);
             mbar_init(&empty[s], 2);
             mbar_init(&v_ready[s], 1);
         }
@@ -438,16 +443,17 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                     const unsigned bytes = (unsigned)__popc(__ballot_sync(0xffffffffu, want)) << (box_shift + 7);
                     for (int kv = 0; ok && kv < 2; ++kv) {
                         const int s = e % NST;
+                        uint64_t *full = kv ? &full_v[s] : &full_k[s];
                         bool go = true;
                         if (lane == 0) {
                             go = mbar_wait(&empty[s], ((unsigned)(e / NST) & 1u) ^ 1u);
-                            if (go) mbar_expect_tx(&full[s], bytes);
+                            if (go) mbar_expect_tx(full, bytes);
                         }
                         ok = __all_sync(0xffffffffu, go);
                         if (!ok) break;
                         if (want)
                             tma_load_2d(ring + s * kPtTile + half * kPtHalf + (sub << (box_shift + 7)),
-                                        kv ? &a.tm_v : &a.tm_k, 64 * half, row, &full[s]);
+                                        kv ? &a.tm_v : &a.tm_k, 64 * half, row, full);
                         ++e;
                     }
                 }
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                        dv0 = umma_desc_lbo(smem_u32(ring), kPtHalf);
         const uint32_t d_o = tm + kPtO + 128u * t, d_s = tm + kPtS + 128u * t;
         int sk = 0, sv = 1;                // ring stages of the next K and V
-        unsigned lk = 0, lv = 0;           // and their laps (v_ready has a phase per two laps)
+        unsigned lk = 0, lv = 0;           // and their laps
         unsigned n_p = 0, n_q = 0;         // phases of p_full, and of q_ready / o_empty
         bool ok = true;
         auto wait = [&](uint64_t *bar, unsigned parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
@@ -513,14 +519,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             const bool mine = __shfl_sync(0xffffffffu, (int)(t == 0 || w.x.ntok > a.tb), 0);
             const int n = __shfl_sync(0xffffffffu, w.n, 0);
             if (mine) wait(&q_ready[t], n_q);
-            wait(&full[sk], lk);
+            wait(&full_k[sk], lk >> 1);
             if (ok && mine) issue_s(0), issue_s(1);
             if (ok && !mine) commit(&empty[sk]);  // (an item of one tile: its stages need this warp's word too)
             step(sk, lk);
             for (int i = 0; ok && i < n; ++i) {
                 const bool more = i < n - 1;
                 wait(&v_ready[sv], lv >> 1);
-                if (more) wait(&full[sk], lk);
+                if (more) wait(&full_k[sk], lk >> 1);
                 if (mine) {
                     if (i == 0) wait(&o_empty[t], n_q ^ 1u);
 #pragma unroll
@@ -544,17 +550,24 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         commit(fin);
         if (!mbar_wait(fin, 0)) *s_fail = 1;
     } else if (busy && warp == 2) {
-        // ---- values of keys that no row sees become zero ----
+        // ---- values of keys that no row sees become zero; the next segment's queries are
+        //      brought into L2 while this one's keys are worked on ----
         int e = 1;
         bool ok = true;
         do {
             const PtItem &x = w.x;
+            PtWalk nx = w;
+            if (nx.next(a)) {
+                const int size = QF32 ? 4 : 2, lines = size;  // 128-byte lines of a row
+                for (int k = lane; k < nx.x.ntok * a.g * lines; k += 32) {
+                    const int rk = k / lines;
+                    const int64_t o = (nx.x.row0 + rk / a.g) * a.q_ts + (nx.j * a.g + rk % a.g) * a.q_hs;
+                    prefetch_l2(static_cast<const char *>(a.q) + o * size + 128 * (k % lines));
+                }
+            }
             for (int i = w.i0; ok && i < w.i0 + w.n; ++i, e += 2) {
-                // the key tile first: copies may land out of order, and a stage's
-                // parity names its lap only once the lap before has landed
-                const int s = e % NST, sk = (e - 1) % NST;
-                ok = __all_sync(0xffffffffu, !*s_fail && mbar_wait(&full[sk], (unsigned)((e - 1) / NST) & 1u) &&
-                                                 mbar_wait(&full[s], (unsigned)(e / NST) & 1u));
+                const int s = e % NST;
+                ok = __all_sync(0xffffffffu, mbar_wait(&full_v[s], (unsigned)((e / NST) >> 1) & 1u));
                 if (!ok) break;
                 const int k0 = x.tile(i) * kPtKeys;
                 if (!(k0 + kPtKeys <= x.len && (k0 >= x.lo || k0 + kPtKeys <= x.sk))) {
@@ -598,35 +611,35 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             const int all_p = __reduce_min_sync(0xffffffffu, live ? p : 0x7fffffff);
             const int all_lo = __reduce_max_sync(0xffffffffu, live ? lo : 0);
 
-            // q row into shared memory, 128-byte swizzle
+            // the warp's 32 rows of q into shared memory, 128-byte swizzle: a row (fp32) or two
+            // (bf16) per load, the lanes side by side
             {
-                unsigned char *dst = s_q + t * SM::QPARTS * kPtTile + r * 128;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {  // chunks of 8 values
-                    unsigned char *d = dst + (c >> 3) * kPtHalf + (((c & 7) ^ (r & 7)) << 4);
-                    if (QF32) {
-                        float4 f0 = make_float4(0.f, 0.f, 0.f, 0.f), f1 = f0;
-                        if (live) {
-                            const float4 *qp = reinterpret_cast<const float4 *>(
-                                static_cast<const float *>(a.q) + row * a.q_ts + head * a.q_hs + 8 * c);
-                            f0 = qp[0];
-                            f1 = qp[1];
-                        }
-                        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                        uint32_t h[4], l[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            h[y] = pack_bf16x2(f[2 * y], f[2 * y + 1]);
-                            l[y] = pack_bf16x2(f[2 * y] - bf16lo(h[y]), f[2 * y + 1] - bf16hi(h[y]));
-                        }
-                        *reinterpret_cast<uint4 *>(d) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4 *>(d + kPtTile) = make_uint4(l[0], l[1], l[2], l[3]);
-                    } else {
+                unsigned char *dst = s_q + t * SM::QPARTS * kPtTile;
+                const long long off = live ? row * a.q_ts + head * a.q_hs : -1;
+                if (QF32) {
+                    const int half = lane >> 4, c = (lane & 15) >> 1;
+#pragma unroll 8
+                    for (int k = 0; k < 32; ++k) {
+                        const long long o = __shfl_sync(0xffffffffu, off, k);
+                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (o >= 0) f = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + o)[lane];
+                        const int rk = 32 * qd + k;
+                        unsigned char *d = dst + half * kPtHalf + rk * 128 + ((c ^ (rk & 7)) << 4) + 8 * (lane & 1);
+                        const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
+                        *reinterpret_cast<uint2 *>(d) = make_uint2(h0, h1);
+                        *reinterpret_cast<uint2 *>(d + kPtTile) =
+                            make_uint2(pack_bf16x2(f.x - bf16lo(h0), f.y - bf16hi(h0)),
+                                       pack_bf16x2(f.z - bf16lo(h1), f.w - bf16hi(h1)));
+                    }
+                } else {
+                    const int half = (lane & 15) >> 3, c = lane & 7;
+#pragma unroll 8
+                    for (int k = 0; k < 32; k += 2) {
+                        const int rk = k + (lane >> 4);
+                        const long long o = __shfl_sync(0xffffffffu, off, rk);
                         uint4 u = make_uint4(0, 0, 0, 0);
-                        if (live)
-                            u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + row * a.q_ts +
-                                                                 head * a.q_hs + 8 * c);
-                        *reinterpret_cast<uint4 *>(d) = u;
+                        if (o >= 0) u = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + o)[lane & 15];
+                        *reinterpret_cast<uint4 *>(dst + half * kPtHalf + (32 * qd + rk) * 128 + ((c ^ (rk & 7)) << 4)) = u;
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -769,7 +782,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     if (*s_fail && threadIdx.x == 0) {
         record_error(8u);
         const int e1 = *s_issued;
-        for (int e = e1 > NST ? e1 - NST : 0; e < e1; ++e) mbar_wait(&full[e % NST], (unsigned)(e / NST) & 1u);
+        for (int e = e1 > NST ? e1 - NST : 0; e < e1; ++e) mbar_wait(e & 1 ? &full_v[e % NST] : &full_k[e % NST], (unsigned)((e / NST) >> 1) & 1u);
     }
     __syncthreads();
     if (warp == 1) {
