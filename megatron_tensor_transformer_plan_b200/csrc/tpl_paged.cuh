@@ -75,15 +75,19 @@ __device__ __forceinline__ float ex2(float x) {
 // (RoFormer's rotation, half-split pairing; TPL_ROPE) or is the identity.
 // A pass over memory: every value is read once and written once, so HBM is
 // the bound and the rotation has to stay hidden behind the loads.  One CTA
-// takes one token (or a part of its heads when there are few tokens): its 64
-// angles are formed once, in turns and in fp64 (far positions are thousands
-// of turns, of which only the fraction counts), shared by all heads, and
-// evaluated while the CTA's first loads are in flight.  A work item is 16
-// bytes of a row's first half with the 16 bytes of the second half they are
-// turned with.
+// takes one token, several when a token has few heads, or a part of its heads
+// when there are few tokens: the 64 angles of a token are formed once, in turns
+// and in fp64 (far positions are thousands of turns, of which only the fraction
+// counts), shared by all heads, and evaluated while the CTA's first loads are
+// in flight.  A work item is 16 bytes of a row's first half with the 16 bytes
+// of the second half they are turned with.
+// 4 warps with up to 6 items a thread measured best (bf16, 64/8 heads, 16k
+// tokens: 105 us against 119 us with 8 warps and 111 us with up to 8 items;
+// 32/32 heads: 96, 103 and 101 us).
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendItems = 4;  // items in flight per thread
+constexpr int kAppendThreads = 128;
+constexpr int kAppendItems = 6;   // items in flight per thread
+constexpr int kAppendTokens = 8;  // tokens per CTA at most
 
 struct AppendArgs {
     PagedView v;
@@ -93,7 +97,8 @@ struct AppendArgs {
     __nv_bfloat16 *kc, *vc;
     int nq;                  // query heads (0: no q)
     int rope;
-    int items_per_cta;
+    int tokens_per_cta;      // 1 when a token's items are spread over several CTAs
+    int items_per_cta;       // of a token
     double turns[64];        // rope_base^(-2e/128) / (2 pi)
 };
 
@@ -135,29 +140,42 @@ struct AppendIo<__nv_bfloat16> {
     }
 };
 
-template <typename T>
+// MANY: several tokens per CTA.
+template <typename T, bool MANY>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendArgs a) {
     using Io = AppendIo<T>;
     constexpr int N = Io::N;
     constexpr int IPH = 64 / N;  // items per head
-    __shared__ float s_cos[64], s_sin[64];
-    __shared__ int s_seq;
-    const int tok = blockIdx.x;
+    constexpr int TOKENS = MANY ? kAppendTokens : 1;
+    __shared__ float s_cos[TOKENS][64], s_sin[TOKENS][64];
+    __shared__ int s_seq[TOKENS], s_pos[TOKENS];
+    __shared__ int64_t s_row[TOKENS];  // the token's slot in the pages of head 0; -1: none
+    const int tok0 = MANY ? blockIdx.x * a.tokens_per_cta : blockIdx.x;
+    const int ntok = MANY ? min(a.tokens_per_cta, a.v.n_tokens - tok0) : 1;
     const int nkv = a.v.nkv;
-    const int items = (a.nq + 2 * nkv) * IPH;
-    const int i0 = blockIdx.y * a.items_per_cta, i1 = min(items, i0 + a.items_per_cta);
-    if (threadIdx.x == 0) s_seq = -1;
+    const int per_tok = (a.nq + 2 * nkv) * IPH;
+    const int i0 = blockIdx.y * a.items_per_cta, i1 = MANY ? ntok * per_tok : min(per_tok, i0 + a.items_per_cta);
+    if (threadIdx.x < TOKENS) s_seq[threadIdx.x] = -1;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
 
+    // item -> token of the CTA, head (query, key, value), first of its values
+    auto split = [&](int item, int &tk, int &h, int &e) {
+        tk = MANY ? item / per_tok : 0;
+        if (MANY) item -= tk * per_tok;
+        h = item / IPH;
+        e = item % IPH * N;
+    };
     auto source = [&](int item) -> const uint4 * {
-        const int h = item / IPH, c = item % IPH;
+        int tk, h, e;
+        split(item, tk, h, e);
+        const int64_t tok = tok0 + tk;
         const T *p;
         if (h < a.nq) p = static_cast<const T *>(a.q) + tok * a.q_ts + h * a.q_hs;
         else if (h < a.nq + nkv) p = static_cast<const T *>(a.k) + tok * a.k_ts + (h - a.nq) * a.k_hs;
         else p = static_cast<const T *>(a.kv) + tok * a.v_ts + (h - a.nq - nkv) * a.v_hs;
-        return reinterpret_cast<const uint4 *>(p + c * N);
+        return reinterpret_cast<const uint4 *>(p + e);
     };
     uint4 lo[kAppendItems], hi[kAppendItems];
 #pragma unroll
@@ -170,30 +188,48 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         }
     }
 
-    // the token's sequence: every thread looks at some of them
+    // the tokens' sequences: every thread looks at some of them
     if (a.v.q_start) {
-        for (int b = threadIdx.x; b < a.v.n_seqs; b += kAppendThreads)
-            if (a.v.q_start[b] <= tok && tok < a.v.q_start[b + 1]) atomicMax(&s_seq, b);
-    } else if (threadIdx.x == 0) {
-        s_seq = tok;
+        for (int b = threadIdx.x; b < a.v.n_seqs; b += kAppendThreads) {
+            const int first = max(a.v.q_start[b], tok0), end = min(a.v.q_start[b + 1], tok0 + ntok);
+            for (int x = first; x < end; ++x) atomicMax(&s_seq[x - tok0], b);
+        }
+    } else if (threadIdx.x < ntok) {
+        s_seq[threadIdx.x] = tok0 + threadIdx.x;
     }
     __syncthreads();
-    const int b = s_seq;
-    if (b < 0) return;  // a row behind the last sequence
-    int start, count;
-    paged_tokens(a.v, b, start, count);
-    const int pos = paged_len(a.v, b) - count + (tok - start);
-    if (count == 0 || pos < 0) return;  // an inactive sequence
-    if (a.rope && threadIdx.x < 64) {
-        const double turn = (double)pos * a.turns[threadIdx.x];
-        float s, c;
-        sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
-        s_cos[threadIdx.x] = c;
-        s_sin[threadIdx.x] = s;
+    // position and slot of token x; -1: a row of no sequence or an inactive one, and no page
+    auto place = [&](int x, int &pos, int64_t &row) {
+        const int b = s_seq[x];
+        pos = -1;
+        row = -1;
+        if (b < 0) return;
+        int start, count;
+        paged_tokens(a.v, b, start, count);
+        if (count > 0) pos = paged_len(a.v, b) - count + (tok0 + x - start);
+        if (pos < 0) return;
+        row = paged_row(a.v, b, pos >> a.v.page_shift, 0);  // head 0 of shard 0
+        if (row >= 0) row += pos & ((1 << a.v.page_shift) - 1);
+    };
+    int pos0 = 0;
+    int64_t row0 = 0;
+    if (MANY) {
+        if (threadIdx.x < ntok) place(threadIdx.x, s_pos[threadIdx.x], s_row[threadIdx.x]);
+        __syncthreads();
+    } else {
+        place(0, pos0, row0);
+        if (pos0 < 0) return;
     }
-    const int slot = pos & ((1 << a.v.page_shift) - 1);
-    const int64_t page_row = paged_row(a.v, b, pos >> a.v.page_shift, 0);  // head 0 of shard 0
-    __syncthreads();
+    if (a.rope) {
+        for (int x = threadIdx.x; x < ntok * 64; x += kAppendThreads) {
+            const double turn = (double)(MANY ? s_pos[x / 64] : pos0) * a.turns[x % 64];
+            float s, c;
+            sincospif((float)(2.0 * (turn - rint(turn))), &s, &c);
+            s_cos[x / 64][x % 64] = c;
+            s_sin[x / 64][x % 64] = s;
+        }
+        __syncthreads();
+    }
 
     for (int base = i0 + threadIdx.x; base < i1; base += kAppendItems * kAppendThreads) {
         if (base != i0 + (int)threadIdx.x) {
@@ -211,27 +247,30 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         for (int r = 0; r < kAppendItems; ++r) {
             const int item = base + r * kAppendThreads;
             if (item >= i1) break;
-            const int h = item / IPH, e = (item % IPH) * N;
+            int tk, h, e;
+            split(item, tk, h, e);
+            if (MANY && s_pos[tk] < 0) continue;
+            const int64_t slot = MANY ? s_row[tk] : row0;
             float x[N], y[N];
             Io::unpack(lo[r], x);
             Io::unpack(hi[r], y);
             if (a.rope && h < a.nq + nkv) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float c = s_cos[e + i], s = s_sin[e + i], x0 = x[i];
+                    const float c = s_cos[tk][e + i], s = s_sin[tk][e + i], x0 = x[i];
                     x[i] = x0 * c - y[i] * s;
                     y[i] = y[i] * c + x0 * s;
                 }
             }
             if (h < a.nq) {
-                T *p = static_cast<T *>(a.q_out) + tok * a.qo_ts + h * a.qo_hs + e;
+                T *p = static_cast<T *>(a.q_out) + (int64_t)(tok0 + tk) * a.qo_ts + h * a.qo_hs + e;
                 *reinterpret_cast<uint4 *>(p) = Io::pack(x);
                 *reinterpret_cast<uint4 *>(p + 64) = Io::pack(y);
-            } else if (page_row >= 0) {
+            } else if (slot >= 0) {
                 const bool is_k = h < a.nq + nkv;
                 const int j = h - a.nq - (is_k ? 0 : nkv);
                 const int sh = j / a.v.nkv_s, jl = j % a.v.nkv_s;
-                const int64_t row = page_row + ((((int64_t)sh * a.v.n_pages * a.v.nkv_s) + jl) << a.v.page_shift) + slot;
+                const int64_t row = slot + ((((int64_t)sh * a.v.n_pages * a.v.nkv_s) + jl) << a.v.page_shift);
                 __nv_bfloat16 *p = (is_k ? a.kc : a.vc) + row * 128 + e;
                 Io::store_bf16(p, x);
                 Io::store_bf16(p + 64, y);

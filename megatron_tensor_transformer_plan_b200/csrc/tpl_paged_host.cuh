@@ -86,15 +86,19 @@ int paged_append(const tpl_plan *p, const tpl_paged_kv *kv, const PagedView &vie
     const bool f32 = k->type == TPL_F32;
     const int sms = num_sms_current();
     if (sms <= 0) return TPL_ECUDA;
-    // a token per CTA; with few tokens its heads are spread over more CTAs, one
-    // item per thread, so that a single token does not wait on one SM
+    // a token per CTA, or as many as fill its threads; with few tokens a token's heads
+    // are spread over more CTAs, one item per thread, so that it does not wait on one SM
     const int items = (a.nq + 2 * view.nkv) * (f32 ? 16 : 8);
     const int parts = (items + kAppendThreads - 1) / kAppendThreads;
     const bool spread = (int64_t)view.n_tokens * parts <= 4 * sms;
     a.items_per_cta = spread ? kAppendThreads : items;
-    const dim3 grid((unsigned)view.n_tokens, (unsigned)((items + a.items_per_cta - 1) / a.items_per_cta));
-    return cuda_rc(f32 ? launch_pdl(paged_append_kernel<float>, grid, kAppendThreads, 0, st, a)
-                       : launch_pdl(paged_append_kernel<__nv_bfloat16>, grid, kAppendThreads, 0, st, a));
+    a.tokens_per_cta = spread ? 1 : std::max(1, std::min(kAppendTokens, kAppendItems * kAppendThreads / items));
+    const dim3 grid((unsigned)((view.n_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta),
+                    (unsigned)((items + a.items_per_cta - 1) / a.items_per_cta));
+    auto go = [&](auto *kernel) { return cuda_rc(launch_pdl(kernel, grid, kAppendThreads, 0, st, a)); };
+    if (a.tokens_per_cta > 1)
+        return f32 ? go(paged_append_kernel<float, true>) : go(paged_append_kernel<__nv_bfloat16, true>);
+    return f32 ? go(paged_append_kernel<float, false>) : go(paged_append_kernel<__nv_bfloat16, false>);
 }
 
 struct PagedCall {

@@ -43,6 +43,8 @@ APPEND = [
     (24, 8, 8, 128, [500, 17, 1, 130], [123, 20, 1, 2], torch.float32, True),
     (48, 4, 1, 16, [900, 31], [513, 31], torch.bfloat16, False),
     (64, 8, 8, 64, [65, 129, 700] * 20, None, torch.float32, False),
+    (8, 1, 1, 32, [800, 3, 1400, 0], [700, 5, 1301, 2], torch.float32, True),
+    (1, 1, 1, 16, [40] * 700, None, torch.bfloat16, True),
 ]
 
 
