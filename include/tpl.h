@@ -437,7 +437,10 @@ int tpl_paged_append(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_pag
  * type; lse: fp32 [n_tokens][n_q] or NULL, the natural logarithm of the
  * softmax denominator.  A token that sees no key gets o = 0, lse = -inf.
  * Logits are q.k / sqrt(d); q is TPL_F32 or TPL_BF16 (fp32 queries cost the
- * prompts a second product).  With q_start (prompts) a plan with
+ * prompts a second product).  What lies in slots that no token of the call sees
+ * has no effect, whatever it is; a NaN or an infinity among the values of a key
+ * that some token of a prompt (or some sequence behind a shared prefix) sees
+ * may also reach the tokens that do not see it.  With q_start (prompts) a plan with
  * TPL_FP32_WEIGHTS is TPL_EUNSUPPORTED, as in prefill.  The same inputs give
  * the same bits. */
 int tpl_paged_attn(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,
