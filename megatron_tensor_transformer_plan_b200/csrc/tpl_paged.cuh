@@ -21,6 +21,16 @@ struct PagedView {
     int32_t max_pages, n_pages, page_shift, n_seqs, n_tokens, nkv, nkv_s;
 };
 
+// The work of a launch, U units, is cut into G equal ranges, one per CTA: the
+// first unit of range c, and the range that unit x lies in (the last c with
+// U c / G <= x).  Divisions of 64 bits take some hundred cycles, those of 32 a
+// few tens, and most launches are small.
+__device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+__device__ __forceinline__ int64_t paged_cut(int64_t U, int G, int c) { return paged_div(U * c, G); }
+__device__ __forceinline__ int paged_cta_of(int64_t U, int G, int64_t x) { return (int)paged_div((x + 1) * G - 1, U); }
+
 // Keys of sequence b.
 __device__ __forceinline__ int paged_len(const PagedView &v, int b) {
     const int len = v.kv_len[b];

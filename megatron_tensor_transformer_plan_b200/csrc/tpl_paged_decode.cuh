@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         return;
     }
 
-    const int64_t u0 = am_start(U, G, cta), u1 = am_start(U, G, cta + 1);
+    const int64_t u0 = paged_cut(U, G, cta), u1 = paged_cut(U, G, cta + 1);
     const int n = (int)(u1 - u0);
     // the sequence of unit u: the last one that begins at or before it
     auto seq_of = [&](int64_t u) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             PdWalk w;
             w.open(a, s_len, seq_of(u));
             const int64_t rel = u - s_start[w.b];
-            w.j = rel >> 32 ? (int)(rel / w.sp.nblk) : (int)((uint32_t)rel / (uint32_t)w.sp.nblk);
+            w.j = (int)paged_div(rel, w.sp.nblk);
             const int key = w.sp.block((int)(rel - (int64_t)w.j * w.sp.nblk)) * kPdKeys + ((lane % nsub) << box_shift);
             const bool want = i0 + lane / nsub < n && key < w.sp.len && (key + (1 << box_shift) > w.sp.lo || key < w.sp.sk);
             if (!want) return -1;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         int64_t pair_start = s_start[w.b];
         {
             const int64_t rel = u0 - pair_start;
-            w.j = (int)(rel / w.sp.nblk);
+            w.j = (int)paged_div(rel, w.sp.nblk);
             pair_start += (int64_t)w.j * w.sp.nblk;
         }
         int i = 0;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         int64_t pair_start = s_start[w.b];
         {
             const int64_t rel = u0 - pair_start;
-            w.j = (int)(rel / w.sp.nblk);
+            w.j = (int)paged_div(rel, w.sp.nblk);
             pair_start += (int64_t)w.j * w.sp.nblk;
         }
         // the queries of segment seg: rows of hi parts, then of lo parts
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             }
             meet();
             const bool whole = pair_start >= u0 && pair_end <= u1;
-            const int cf = whole ? cta : am_cta_of(U, G, pair_start);
+            const int cf = whole ? cta : paged_cta_of(U, G, pair_start);
             auto emit = [&](int hrow, const float4 &num, float M, float den) {
                 const int64_t row = (int64_t)w.b * a.nq + w.j * a.g + hrow;
                 if (a.own_o) {
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 }
             }
             if (!whole) {
-                const int n_p = am_cta_of(U, G, pair_end - 1) - cf + 1;
+                const int n_p = paged_cta_of(U, G, pair_end - 1) - cf + 1;
                 __threadfence();
                 meet();
                 if (tid == 0) {
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                     float *s_mlp = s_o + slot * (SM::STATE / 4);  // [n_p][g][2]
                     float *s_w = s_mlp + 2 * GM * kPagedMaxCtas;  // [n_p][GM]
                     // CTA cf's part of the pair is its second segment when its range begins before the pair
-                    const int part0 = 2 * cf + (am_start(U, G, cf) < pair_start ? 1 : 0);
+                    const int part0 = 2 * cf + (paged_cut(U, G, cf) < pair_start ? 1 : 0);
                     auto part_of = [&](int x) { return x == 0 ? part0 : 2 * (cf + x); };
                     for (int x = tid; x < n_p * a.g; x += kPdMergeWarps * 32) {
                         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) +

@@ -255,13 +255,16 @@ int paged_shared(const PagedCall &c, int shared) {
     int rc = paged_prompt_args(c, &a, &grid);
     if (rc != TPL_OK) return rc;
     a.shared = shared;
+    // The CTAs: as many per item as there are, so that no CTA has parts of two (64 sequences,
+    // 8192 keys: 16 items, 144 CTAs rather than 148), when there are more CTAs than items.
+    const int64_t items = (int64_t)((c.v.n_tokens + 2 * a.tb - 1) / (2 * a.tb)) * c.v.nkv;
+    const int64_t U = items * ((shared + kPtKeys - 1) / kPtKeys);
+    a.G = (int)std::min<int64_t>(grid, (U + kPtMinTiles - 1) / kPtMinTiles);
+    if (items <= a.G) a.G = (int)(a.G / items * items);
+    s.G = a.G;
     rc = c.q->type == TPL_F32 ? paged_prompt_go<true>(a, grid, c.st) : paged_prompt_go<false>(a, grid, c.st);
     if (rc == TPL_OK) rc = paged_decode(c, 0, 0, shared, true);
     if (rc != TPL_OK) return rc;
-    // the CTAs the kernel cuts the prefix into
-    const int64_t items = (c.v.n_tokens + 2 * a.tb - 1) / (2 * a.tb);
-    const int64_t U = items * c.v.nkv * ((shared + kPtKeys - 1) / kPtKeys);
-    s.G = (int)std::min<int64_t>(grid, (U + kPtMinTiles - 1) / kPtMinTiles);
     s.own_o = reinterpret_cast<const float *>(c.ws + c.L.own_o);
     s.own_ml = reinterpret_cast<const float *>(c.ws + c.L.own_ml);
     const int64_t rows = (int64_t)c.v.n_tokens * a.nq;

@@ -76,6 +76,7 @@ struct PagedPromptArgs {
     // CTA's first segment); prefix: slot item + c
     float *part_o, *part_ml;
     int part_rows;           // rows per slot
+    int G;                   // CTAs that take part (0: decided at the device)
     int4 *cut;               // [grid] prompts: {first token, row tokens, kv head, parts} of the item CTA c is the first of
 };
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ int pt_window(const PagedPromptArgs &a, int p) {
     return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
 }
 
-__device__ __forceinline__ PtItem pt_item(const PagedPromptArgs &a, int b, int start, int count, int it) {
+__device__ __forceinline__ PtItem pt_item(const PagedPromptArgs &a, int len, int start, int count, int it) {
     PtItem x;
     const int t0 = it * 2 * a.tb;
     x.row0 = start + t0;
@@ -107,7 +108,7 @@ __device__ __forceinline__ PtItem pt_item(const PagedPromptArgs &a, int b, int s
         x.ntk = (a.shared + kPtKeys - 1) / kPtKeys;
         return x;
     }
-    x.p0 = paged_len(a.v, b) - count + t0;
+    x.p0 = len - count + t0;
     x.len = max(0, x.p0 + x.ntok);
     x.lo = pt_window(a, x.p0);
     x.sk = min(a.sinks, x.lo);
@@ -122,7 +123,7 @@ __device__ __forceinline__ PtItem pt_item(const PagedPromptArgs &a, int b, int s
 struct PtWalk {
     int64_t u, u1;
     int j, b, it;        // kv head, sequence, item of the sequence
-    int start, count;    // its tokens
+    int start, count, len;  // its tokens and keys
     int done;            // key tiles of the item before u
     int idx;             // items before this one, over all kv heads (prefix mode)
     PtItem x;
@@ -130,7 +131,7 @@ struct PtWalk {
     bool first;          // the CTA's first segment
 
     __device__ __forceinline__ void open(const PagedPromptArgs &a) {
-        x = pt_item(a, b, start, count, it);
+        x = pt_item(a, len, start, count, it);
         i0 = done;
         n = (int)min((int64_t)(x.ntk - done), u1 - u);
     }
@@ -138,8 +139,10 @@ struct PtWalk {
         if (a.shared > 0) {
             start = 0;
             count = a.v.n_tokens;
+            len = 0;
         } else {
             paged_tokens(a.v, b, start, count);
+            len = paged_len(a.v, b);
         }
     }
     __device__ __forceinline__ bool next(const PagedPromptArgs &a) {
@@ -253,9 +256,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
     volatile int *s_fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_issued = const_cast<int *>(s_fail) + 1;
-    int *s_where = s_issued + 1;          // [4] start of this CTA's range: j, b, item, tiles before
-    long long *s_sum = reinterpret_cast<long long *>((reinterpret_cast<uintptr_t>(s_where + 4) + 7) & ~(uintptr_t)7);
-    static_assert((4 * NST + 17) * 8 + 40 + 16 + kPtThreads / 32 * 8 <= SM::BAR, "barrier area");
+    int *s_where = s_issued + 1;          // [7] start of this CTA's range: j, b, item, tiles before; b's tokens and keys
+    long long *s_sum = reinterpret_cast<long long *>((reinterpret_cast<uintptr_t>(s_where + 7) + 7) & ~(uintptr_t)7);
+    static_assert((4 * NST + 17) * 8 + 56 + 16 + kPtThreads / 32 * 8 <= SM::BAR, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
@@ -293,11 +296,15 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's range of the key tiles: each thread sums a run of items ----
+    // ---- this CTA's range of the key tiles ----
     int64_t U1;  // key tiles of one kv head
-    {
+    if (a.shared > 0) {
+        U1 = (int64_t)pt_items(a, a.v.n_tokens) * ((a.shared + kPtKeys - 1) / kPtKeys);
+    } else {
+        // the sequences' items, tokens and keys; then each thread sums a run of items
+        const int ns = a.v.n_seqs;
         int *s_item = reinterpret_cast<int *>(ring);  // [n_seqs + 1] items before sequence b
-        const int ns = a.shared > 0 ? 1 : a.v.n_seqs;
+        int *s_start = s_item + kPagedMaxSeqs + 1, *s_count = s_start + kPagedMaxSeqs, *s_len = s_count + kPagedMaxSeqs;
         constexpr int PT = (kPagedMaxSeqs + kPtThreads - 1) / kPtThreads;
         const int per = (ns + kPtThreads - 1) / kPtThreads;
         int mine[PT], cnt = 0;
@@ -306,8 +313,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             const int b = threadIdx.x * per + x;
             mine[x] = 0;
             if (x < per && b < ns) {
-                int start = 0, count = a.v.n_tokens;
-                if (a.shared == 0) paged_tokens(a.v, b, start, count);
+                int start, count;
+                const int len = paged_len(a.v, b);
+                paged_tokens(a.v, b, start, count);
+                s_start[b] = start;
+                s_count[b] = count;
+                s_len[b] = len;
                 mine[x] = pt_items(a, count);
             }
             cnt += mine[x];
@@ -348,14 +359,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                 if (s_item[mid] <= k0) l = mid;
                 else r = mid - 1;
             }
-            int b = l, start = 0, count = a.v.n_tokens;
-            if (a.shared == 0) paged_tokens(a.v, b, start, count);
+            int b = l;
             for (int k = k0; k < k1; ++k) {
-                while (k >= s_item[b + 1]) {
-                    ++b;
-                    if (a.shared == 0) paged_tokens(a.v, b, start, count);
-                }
-                visit(b, k - s_item[b], pt_item(a, b, start, count, k - s_item[b]).ntk);
+                while (k >= s_item[b + 1]) ++b;
+                visit(b, k - s_item[b], pt_item(a, s_len[b], s_start[b], s_count[b], k - s_item[b]).ntk);
             }
         };
         long long tiles = 0;
@@ -368,8 +375,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         const int64_t U = U1 * a.v.nkv;
         const int G = (int)min((int64_t)gridDim.x, max((int64_t)1, (U + kPtMinTiles - 1) / kPtMinTiles));
         if (cta < G && U > 0) {
-            const int64_t u0 = am_start(U, G, cta);
-            const int j = (int)(u0 / U1);
+            const int64_t u0 = paged_cut(U, G, cta);
+            const int j = (int)paged_div(u0, U1);
             const int64_t rel = u0 - j * U1;
             if (rel >= before && rel < before + tiles) {
                 long long t = before;
@@ -379,6 +386,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                         s_where[1] = b;
                         s_where[2] = it;
                         s_where[3] = (int)(rel - t);
+                        s_where[4] = s_start[b];
+                        s_where[5] = s_count[b];
+                        s_where[6] = s_len[b];
                     }
                     t += ntk;
                 });
@@ -388,21 +398,33 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         __syncthreads();
     }
     const int64_t U = U1 * a.v.nkv;
-    const int G = (int)min((int64_t)gridDim.x, max((int64_t)1, (U + kPtMinTiles - 1) / kPtMinTiles));
+    const int G = a.G > 0 ? a.G : (int)min((int64_t)gridDim.x, max((int64_t)1, (U + kPtMinTiles - 1) / kPtMinTiles));
     const bool busy = cta < G && U > 0;
     if (threadIdx.x == 128 && a.cut) a.cut[cta] = make_int4(0, 0, 0, 0);  // the thread that may fill it in below
 
     PtWalk w;
     if (busy) {
-        w.u = am_start(U, G, cta);
-        w.u1 = am_start(U, G, cta + 1);
-        w.j = s_where[0];
-        w.b = s_where[1];
-        w.it = s_where[2];
-        w.done = s_where[3];
+        w.u = paged_cut(U, G, cta);
+        w.u1 = paged_cut(U, G, cta + 1);
         w.first = true;
-        w.tokens(a);
-        w.idx = w.j * pt_items(a, a.v.n_tokens) + w.it;  // (prefix mode: one pseudo sequence)
+        if (a.shared > 0) {
+            const int items = pt_items(a, a.v.n_tokens), NT = (a.shared + kPtKeys - 1) / kPtKeys;
+            w.idx = (int)paged_div(w.u, NT);
+            w.done = (int)(w.u - (int64_t)w.idx * NT);
+            w.j = w.idx / items;
+            w.it = w.idx - w.j * items;
+            w.b = 0;
+            w.tokens(a);
+        } else {
+            w.j = s_where[0];
+            w.b = s_where[1];
+            w.it = s_where[2];
+            w.done = s_where[3];
+            w.start = s_where[4];
+            w.count = s_where[5];
+            w.len = s_where[6];
+            w.idx = 0;  // (a prefix's only)
+        }
         w.open(a);
     }
 
@@ -515,7 +537,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                 ++lap;
             }
         };
+        PtWalk nx;  // the segment after this one: looked up while this one is worked on
         do {
+            nx = w;
+            const int another = nx.next(a);
             const bool mine = __shfl_sync(0xffffffffu, (int)(t == 0 || w.x.ntok > a.tb), 0);
             const int n = __shfl_sync(0xffffffffu, w.n, 0);
             if (mine) wait(&q_ready[t], n_q);
@@ -545,7 +570,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                 if (more) step(sk, lk);
             }
             if (mine) ++n_q;
-        } while (ok && __shfl_sync(0xffffffffu, (int)w.next(a), 0));
+            w = nx;
+            if (!__shfl_sync(0xffffffffu, another, 0)) break;
+        } while (ok);
         if (!ok) *s_fail = 1;
         commit(fin);
         if (!mbar_wait(fin, 0)) *s_fail = 1;
@@ -553,11 +580,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         // ---- values of keys that no row sees become zero; the next segment's queries are
         //      brought into L2 while this one's keys are worked on ----
         int e = 1;
-        bool ok = true;
+        bool ok = true, another;
         do {
-            const PtItem &x = w.x;
+            const PtItem x = w.x;
             PtWalk nx = w;
-            if (nx.next(a)) {
+            another = nx.next(a);
+            if (another) {
                 const int size = QF32 ? 4 : 2, lines = size;  // 128-byte lines of a row
                 for (int k = lane; k < nx.x.ntok * a.g * lines; k += 32) {
                     const int rk = k / lines;
@@ -585,7 +613,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&v_ready[s]);
             }
-        } while (ok && w.next(a));
+            w = nx;
+        } while (ok && another);
         if (!ok) *s_fail = 1;
     } else if (busy && warp >= 4) {
         // ---- softmax: thread = row of tile t ----
@@ -594,10 +623,70 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
         const uint32_t scol = tmem + lane_off + kPtS + 128u * t, ocol = tmem + lane_off + kPtO + 128u * t;
         unsigned n_s = 0, seg = 0;  // half tiles (phases of s_full and pv_done) and segments so far
-        bool ok = true;
+        // The warp's 32 rows of a segment's q into shared memory, 128-byte swizzle: a row
+        // (fp32) or two (bf16) per load, the lanes side by side, eight loads at a time.
+        auto load_q = [&](const PtWalk &y) {
+            if (t == 1 && y.x.ntok <= a.tb) return;
+            unsigned char *dst = s_q + t * SM::QPARTS * kPtTile;
+            const int tok = t * a.tb + r / a.g;
+            const bool live = r < a.tb * a.g && tok < y.x.ntok;
+            const long long off = live ? (y.x.row0 + tok) * a.q_ts + (y.j * a.g + r % a.g) * a.q_hs : -1;
+            if (QF32) {
+                const int half = lane >> 4, c = (lane & 15) >> 1;
+#pragma unroll 1
+                for (int k0 = 0; k0 < 32; k0 += 8) {
+                    float4 f[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {  // (rows of no token: any address, then zeros)
+                        const long long o = __shfl_sync(0xffffffffu, off, k0 + k);
+                        f[k] = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + max(o, 0ll))[lane];
+                        if (o < 0) f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int rk = 32 * qd + k0 + k;
+                        unsigned char *d = dst + half * kPtHalf + rk * 128 + ((c ^ k) << 4) + 8 * (lane & 1);
+                        const uint32_t h0 = pack_bf16x2(f[k].x, f[k].y), h1 = pack_bf16x2(f[k].z, f[k].w);
+                        *reinterpret_cast<uint2 *>(d) = make_uint2(h0, h1);
+                        *reinterpret_cast<uint2 *>(d + kPtTile) =
+                            make_uint2(pack_bf16x2(f[k].x - bf16lo(h0), f[k].y - bf16hi(h0)),
+                                       pack_bf16x2(f[k].z - bf16lo(h1), f[k].w - bf16hi(h1)));
+                    }
+                }
+            } else {
+                const int half = (lane & 15) >> 3, c = lane & 7;
+#pragma unroll 1
+                for (int k0 = 0; k0 < 32; k0 += 16) {
+                    uint4 u[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const long long o = __shfl_sync(0xffffffffu, off, k0 + 2 * k + (lane >> 4));
+                        u[k] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + max(o, 0ll))[lane & 15];
+                        if (o < 0) u[k] = make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int rk = 32 * qd + k0 + 2 * k + (lane >> 4);
+                        *reinterpret_cast<uint4 *>(dst + half * kPtHalf + rk * 128 + ((c ^ (rk & 7)) << 4)) = u[k];
+                    }
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready[t]);
+        };
+        bool ok = true, another;
+        PtWalk nx;  // the segment after this one: looked up while this one is worked on
+        load_q(w);
         do {
-            const PtItem &x = w.x;
-            if (t == 1 && x.ntok <= a.tb) continue;  // (continue evaluates the loop's condition)
+            const PtItem x = w.x;
+            nx = w;
+            another = nx.next(a);
+            if (t == 1 && x.ntok <= a.tb) {
+                if (another) load_q(nx);
+                w = nx;
+                continue;  // (evaluates the loop's condition)
+            }
             const int tok = t * a.tb + r / a.g;      // token of the item
             const int head = w.j * a.g + r % a.g;
             const bool live = r < a.tb * a.g && tok < x.ntok;
@@ -611,41 +700,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             const int all_p = __reduce_min_sync(0xffffffffu, live ? p : 0x7fffffff);
             const int all_lo = __reduce_max_sync(0xffffffffu, live ? lo : 0);
 
-            // the warp's 32 rows of q into shared memory, 128-byte swizzle: a row (fp32) or two
-            // (bf16) per load, the lanes side by side
-            {
-                unsigned char *dst = s_q + t * SM::QPARTS * kPtTile;
-                const long long off = live ? row * a.q_ts + head * a.q_hs : -1;
-                if (QF32) {
-                    const int half = lane >> 4, c = (lane & 15) >> 1;
-#pragma unroll 8
-                    for (int k = 0; k < 32; ++k) {
-                        const long long o = __shfl_sync(0xffffffffu, off, k);
-                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (o >= 0) f = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + o)[lane];
-                        const int rk = 32 * qd + k;
-                        unsigned char *d = dst + half * kPtHalf + rk * 128 + ((c ^ (rk & 7)) << 4) + 8 * (lane & 1);
-                        const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
-                        *reinterpret_cast<uint2 *>(d) = make_uint2(h0, h1);
-                        *reinterpret_cast<uint2 *>(d + kPtTile) =
-                            make_uint2(pack_bf16x2(f.x - bf16lo(h0), f.y - bf16hi(h0)),
-                                       pack_bf16x2(f.z - bf16lo(h1), f.w - bf16hi(h1)));
-                    }
-                } else {
-                    const int half = (lane & 15) >> 3, c = lane & 7;
-#pragma unroll 8
-                    for (int k = 0; k < 32; k += 2) {
-                        const int rk = k + (lane >> 4);
-                        const long long o = __shfl_sync(0xffffffffu, off, rk);
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (o >= 0) u = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + o)[lane & 15];
-                        *reinterpret_cast<uint4 *>(dst + half * kPtHalf + (32 * qd + rk) * 128 + ((c ^ (rk & 7)) << 4)) = u;
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_ready[t]);
-            }
             float m = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
 #pragma unroll 1
             for (int i = 0; i < 2 * w.n; ++i) {
@@ -735,46 +789,77 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             const bool done = a.shared == 0 && w.whole();
             const float inv = 1.f / l;
             const int64_t slot = a.shared > 0 ? (int64_t)w.idx + cta : 2 * cta + (w.first ? 0 : 1);
-            float *po = a.part_o + (slot * a.part_rows + 128 * t + r) * 128;
-            if (warp_live) {
+            const int64_t part_row = slot * a.part_rows + 128 * t;
+            // The rows leave through this warp's share of the query tile (8 KB, free until the
+            // next segment's queries come): a thread has a row, a store should have few rows.
+            unsigned char *stage = s_q + t * SM::QPARTS * kPtTile;
+            auto place = [&](int rk, int c) {  // 16-byte chunk c of 16 of row rk of the tile
+                return reinterpret_cast<uint4 *>(stage + (c >> 3) * kPtHalf + rk * 128 + (((c & 7) ^ (rk & 7)) << 4));
+            };
+            if (warp_live && done) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float v[32];
                     tmem_ld32(ocol + 32 * c, v);
                     tmem_ld_wait();
                     tmem_ld_done(v);
-                    if (live && done) {
-                        uint32_t u[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            u[e] = l != 0.f ? pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
-                        uint4 *d = reinterpret_cast<uint4 *>(a.o + (row * a.nq + head) * 128 + 32 * c);
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t u[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) d[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-                    } else if (live) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<float4 *>(po + 32 * c)[e] =
-                                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        for (int y = 0; y < 4; ++y)
+                            u[y] = l != 0.f ? pack_bf16x2(v[8 * e + 2 * y] * inv, v[8 * e + 2 * y + 1] * inv) : 0u;
+                        *place(r, 4 * c + e) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
-                if (live && done) {
-                    if (a.lse) a.lse[row * a.nq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-                } else if (live) {
-                    float *pm = a.part_ml + (slot * a.part_rows + 128 * t + r) * 2;
-                    pm[0] = m;
-                    pm[1] = l;
+                __syncwarp();
+                const long long at = live ? (row * a.nq + head) * 128 : -1;
+#pragma unroll 4
+                for (int k = 0; k < 32; k += 2) {  // two rows of 256 bytes at a time
+                    const int rk = k + (lane >> 4);
+                    const long long o = __shfl_sync(0xffffffffu, at, rk);
+                    if (o >= 0) reinterpret_cast<uint4 *>(a.o + o)[lane & 15] = *place(32 * qd + rk, lane & 15);
                 }
+                if (live && a.lse) a.lse[row * a.nq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            } else if (warp_live) {
+                const unsigned some = __ballot_sync(0xffffffffu, live);
+#pragma unroll 1
+                for (int c2 = 0; c2 < 2; ++c2) {  // 64 dims at a time
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        float v[32];
+                        tmem_ld32(ocol + 64 * c2 + 32 * c, v);
+                        tmem_ld_wait();
+                        tmem_ld_done(v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *place(r, 8 * c + e) = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                                              __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int k = 0; k < 32; k += 2) {
+                        const int rk = k + (lane >> 4);
+                        if (some >> rk & 1u)
+                            reinterpret_cast<uint4 *>(a.part_o + (part_row + 32 * qd + rk) * 128 + 64 * c2)[lane & 15] =
+                                *place(32 * qd + rk, lane & 15);
+                    }
+                    __syncwarp();
+                }
+                if (live) *reinterpret_cast<float2 *>(a.part_ml + (part_row + r) * 2) = make_float2(m, l);
             }
+            __syncwarp();
+            if (another) load_q(nx);
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty[t]);
             // the first CTA of a cut item leaves its place for the join
             if (t == 0 && r == 0 && a.cut && w.i0 == 0 && !done) {
-                const int last = am_cta_of(U, G, w.u + x.ntk - 1);
+                const int last = paged_cta_of(U, G, w.u + x.ntk - 1);
                 a.cut[cta] = make_int4(x.row0, x.ntok | (w.first ? 0 : 1 << 30), w.j, last - cta + 1);
             }
-        } while (w.next(a));
+            w = nx;
+        } while (another);
         if (!ok) *s_fail = 1;
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -876,7 +961,7 @@ __global__ void __launch_bounds__(kPtJoinThreads) paged_shared_join_kernel(const
     const int rr = tok / a.tb * 128 + tok % a.tb * a.g + head % a.g;
     const int64_t NT = (a.shared + kPtKeys - 1) / kPtKeys, idx = (int64_t)j * items + it;
     const int64_t U = NT * items * a.v.nkv;
-    const int cf = am_cta_of(U, g.G, idx * NT), cl = am_cta_of(U, g.G, idx * NT + NT - 1);
+    const int cf = paged_cta_of(U, g.G, idx * NT), cl = paged_cta_of(U, g.G, idx * NT + NT - 1);
     paged_join_row(lane, cl - cf + 1, a.part_ml, a.part_o, [&](int x) { return (idx + cf + x) * a.part_rows + rr; },
                    reinterpret_cast<const float2 *>(g.own_ml) + row,
                    reinterpret_cast<const float4 *>(g.own_o) + row * 32, row, a.o, a.lse);
