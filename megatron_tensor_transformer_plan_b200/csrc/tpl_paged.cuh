@@ -31,9 +31,7 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
 __device__ __forceinline__ int64_t paged_cut(int64_t U, int G, int c) { return paged_div(U * c, G); }
 __device__ __forceinline__ int paged_cta_of(int64_t U, int G, int64_t x) { return (int)paged_div((x + 1) * G - 1, U); }
 
-// Keys of sequence b.
-__device__ __forceinline__ int paged_len(const PagedView &v, int b) {
-    const int len = v.kv_len[b];
+__device__ __forceinline__ int paged_len_ok(const PagedView &v, int len) {
     const int64_t cap = (int64_t)v.max_pages << v.page_shift;
     if (len < 0 || len > cap) {
         record_error(kErrPaged);
@@ -42,21 +40,23 @@ __device__ __forceinline__ int paged_len(const PagedView &v, int b) {
     return len;
 }
 
-// First token row and token count of sequence b.
-__device__ __forceinline__ void paged_tokens(const PagedView &v, int b, int &start, int &count) {
-    if (!v.q_start) {
-        start = b;
-        count = 1;
-        return;
+// Keys of sequence b.
+__device__ __forceinline__ int paged_len(const PagedView &v, int b) { return paged_len_ok(v, v.kv_len[b]); }
+
+// First token row, token count and keys of sequence b (its loads go out together).
+__device__ __forceinline__ void paged_seq(const PagedView &v, int b, int &start, int &count, int &len) {
+    int s = b, e = b + 1;
+    if (v.q_start) {
+        s = v.q_start[b];
+        e = v.q_start[b + 1];
     }
-    const int s = v.q_start[b], e = v.q_start[b + 1];
+    len = paged_len(v, b);
+    start = s;
+    count = e - s;
     if (s < 0 || e < s || e > v.n_tokens) {
         record_error(kErrPaged);
         start = count = 0;
-        return;
     }
-    start = s;
-    count = e - s;
 }
 
 // The pool row (128 values) of page entry `entry` of sequence b for global kv
@@ -214,9 +214,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         pos = -1;
         row = -1;
         if (b < 0) return;
-        int start, count;
-        paged_tokens(a.v, b, start, count);
-        if (count > 0) pos = paged_len(a.v, b) - count + (tok0 + x - start);
+        int start, count, len;
+        paged_seq(a.v, b, start, count, len);
+        if (count > 0) pos = len - count + (tok0 + x - start);
         if (pos < 0) return;
         row = paged_row(a.v, b, pos >> a.v.page_shift, 0);  // head 0 of shard 0
         if (row >= 0) row += pos & ((1 << a.v.page_shift) - 1);

@@ -259,7 +259,7 @@ int paged_shared(const PagedCall &c, int shared) {
     // 8192 keys: 16 items, 144 CTAs rather than 148), when there are more CTAs than items.
     const int64_t items = (int64_t)((c.v.n_tokens + 2 * a.tb - 1) / (2 * a.tb)) * c.v.nkv;
     const int64_t U = items * ((shared + kPtKeys - 1) / kPtKeys);
-    a.G = (int)std::min<int64_t>(grid, (U + kPtMinTiles - 1) / kPtMinTiles);
+    a.G = (int)std::min<int64_t>(grid, (U + kPtMinTilesPrefix - 1) / kPtMinTilesPrefix);
     if (items <= a.G) a.G = (int)(a.G / items * items);
     s.G = a.G;
     rc = c.q->type == TPL_F32 ? paged_prompt_go<true>(a, grid, c.st) : paged_prompt_go<false>(a, grid, c.st);

@@ -47,7 +47,11 @@ constexpr int kPtKeys = 128;                   // keys per tile
 constexpr int kPtHalf = kPtKeys * 128;         // 128 rows x 64 dims, bf16: 16 KB
 constexpr int kPtTile = 2 * kPtHalf;           // one K, V or Q tile: 32 KB
 constexpr int kPtThreads = 384;
-constexpr int kPtMinTiles = 2;                 // key tiles per CTA at least
+// Key tiles per CTA at least.  Prompts: any (3 of 37 tokens after 900 keys: 20.8, 24.4 and
+// 26.6 us with 1, 2 and 4).  A prefix: every cut of an item is one more partial of all its
+// rows to write and join (16 sequences, 4096 keys: 36.4, 34.6, 25.2 and 28.1 us with 1, 2, 4
+// and 6; 5 sequences, 1536 keys: 19.2, 17.7, 18.4 and 21.2 us).
+constexpr int kPtMinTiles = 1, kPtMinTilesPrefix = 4;
 constexpr uint32_t kPtO = 0, kPtS = 256;       // TMEM columns: O of tile t at 128 t, S at 256 + 128 t
 
 template <bool QF32>
@@ -141,8 +145,7 @@ struct PtWalk {
             count = a.v.n_tokens;
             len = 0;
         } else {
-            paged_tokens(a.v, b, start, count);
-            len = paged_len(a.v, b);
+            paged_seq(a.v, b, start, count, len);
         }
     }
     __device__ __forceinline__ bool next(const PagedPromptArgs &a) {
@@ -313,9 +316,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             const int b = threadIdx.x * per + x;
             mine[x] = 0;
             if (x < per && b < ns) {
-                int start, count;
-                const int len = paged_len(a.v, b);
-                paged_tokens(a.v, b, start, count);
+                int start, count, len;
+                paged_seq(a.v, b, start, count, len);
                 s_start[b] = start;
                 s_count[b] = count;
                 s_len[b] = len;
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
         const uint32_t scol = tmem + lane_off + kPtS + 128u * t, ocol = tmem + lane_off + kPtO + 128u * t;
         unsigned n_s = 0, seg = 0;  // half tiles (phases of s_full and pv_done) and segments so far
         // The warp's 32 rows of a segment's q into shared memory, 128-byte swizzle: a row
-        // (fp32) or two (bf16) per load, the lanes side by side, eight loads at a time.
+        // (fp32) or two (bf16) per load, the lanes side by side, sixteen loads at a time.
         auto load_q = [&](const PtWalk &y) {
             if (t == 1 && y.x.ntok <= a.tb) return;
             unsigned char *dst = s_q + t * SM::QPARTS * kPtTile;
@@ -634,18 +636,18 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             if (QF32) {
                 const int half = lane >> 4, c = (lane & 15) >> 1;
 #pragma unroll 1
-                for (int k0 = 0; k0 < 32; k0 += 8) {
-                    float4 f[8];
+                for (int k0 = 0; k0 < 32; k0 += 16) {
+                    float4 f[16];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {  // (rows of no token: any address, then zeros)
+                    for (int k = 0; k < 16; ++k) {  // (rows of no token: any address, then zeros)
                         const long long o = __shfl_sync(0xffffffffu, off, k0 + k);
                         f[k] = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + max(o, 0ll))[lane];
                         if (o < 0) f[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 16; ++k) {
                         const int rk = 32 * qd + k0 + k;
-                        unsigned char *d = dst + half * kPtHalf + rk * 128 + ((c ^ k) << 4) + 8 * (lane & 1);
+                        unsigned char *d = dst + half * kPtHalf + rk * 128 + ((c ^ (k & 7)) << 4) + 8 * (lane & 1);
                         const uint32_t h0 = pack_bf16x2(f[k].x, f[k].y), h1 = pack_bf16x2(f[k].z, f[k].w);
                         *reinterpret_cast<uint2 *>(d) = make_uint2(h0, h1);
                         *reinterpret_cast<uint2 *>(d + kPtTile) =
@@ -656,16 +658,16 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             } else {
                 const int half = (lane & 15) >> 3, c = lane & 7;
 #pragma unroll 1
-                for (int k0 = 0; k0 < 32; k0 += 16) {
-                    uint4 u[8];
+                for (int k0 = 0; k0 < 32; k0 += 32) {
+                    uint4 u[16];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 16; ++k) {
                         const long long o = __shfl_sync(0xffffffffu, off, k0 + 2 * k + (lane >> 4));
                         u[k] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + max(o, 0ll))[lane & 15];
                         if (o < 0) u[k] = make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 16; ++k) {
                         const int rk = 32 * qd + k0 + 2 * k + (lane >> 4);
                         *reinterpret_cast<uint4 *>(dst + half * kPtHalf + rk * 128 + ((c ^ (rk & 7)) << 4)) = u[k];
                     }
