@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             if (lane == 31) s_sum[warp] = inc;
             __syncthreads();
             long long at = inc - val;
-            for (int w = 0; w < warp; ++w) at += s_sum[w];
+#pragma unroll
+            for (int w = 0; w < kPtThreads / 32; ++w) at += w < warp ? s_sum[w] : 0;
             return at;
         };
         int at = (int)scan(cnt);
@@ -798,6 +799,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             auto place = [&](int rk, int c) {  // 16-byte chunk c of 16 of row rk of the tile
                 return reinterpret_cast<uint4 *>(stage + (c >> 3) * kPtHalf + rk * 128 + (((c & 7) ^ (rk & 7)) << 4));
             };
+            const long long at = live ? (row * a.nq + head) * 128 : -1;
+            const unsigned some = __ballot_sync(0xffffffffu, live);
             if (warp_live && done) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -815,37 +818,35 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
                     }
                 }
                 __syncwarp();
-                const long long at = live ? (row * a.nq + head) * 128 : -1;
 #pragma unroll 4
                 for (int k = 0; k < 32; k += 2) {  // two rows of 256 bytes at a time
                     const int rk = k + (lane >> 4);
                     const long long o = __shfl_sync(0xffffffffu, at, rk);
-                    if (o >= 0) reinterpret_cast<uint4 *>(a.o + o)[lane & 15] = *place(32 * qd + rk, lane & 15);
+                    const uint4 u = *place(32 * qd + rk, lane & 15);
+                    if (o >= 0) reinterpret_cast<uint4 *>(a.o + o)[lane & 15] = u;
                 }
                 if (live && a.lse) a.lse[row * a.nq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             } else if (warp_live) {
-                const unsigned some = __ballot_sync(0xffffffffu, live);
 #pragma unroll 1
                 for (int c2 = 0; c2 < 2; ++c2) {  // 64 dims at a time
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        float v[32];
-                        tmem_ld32(ocol + 64 * c2 + 32 * c, v);
-                        tmem_ld_wait();
-                        tmem_ld_done(v);
+                    float v[64];
+                    tmem_ld32(ocol + 64 * c2, v);
+                    tmem_ld32(ocol + 64 * c2 + 32, v + 32);
+                    tmem_ld_wait();
+                    tmem_ld_done(v);
+                    tmem_ld_done(v + 32);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *place(r, 8 * c + e) = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
-                                                              __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        *place(r, e) = make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                                  __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
                     __syncwarp();
-#pragma unroll 4
-                    for (int k = 0; k < 32; k += 2) {
-                        const int rk = k + (lane >> 4);
-                        if (some >> rk & 1u)
-                            reinterpret_cast<uint4 *>(a.part_o + (part_row + 32 * qd + rk) * 128 + 64 * c2)[lane & 15] =
-                                *place(32 * qd + rk, lane & 15);
-                    }
+                    float *po = a.part_o + (part_row + 32 * qd + (lane >> 4)) * 128 + 64 * c2;
+                    uint4 u[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) u[k] = *place(32 * qd + 2 * k + (lane >> 4), lane & 15);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (some >> (2 * k + (lane >> 4)) & 1u) reinterpret_cast<uint4 *>(po + 256 * k)[lane & 15] = u[k];
                     __syncwarp();
                 }
                 if (live) *reinterpret_cast<float2 *>(a.part_ml + (part_row + r) * 2) = make_float2(m, l);
