@@ -440,7 +440,8 @@ int tpl_paged_append(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_pag
  * prompts a second product).  What lies in slots that no token of the call sees
  * has no effect, whatever it is; a NaN or an infinity among the values of a key
  * that some token of a prompt (or some sequence behind a shared prefix) sees
- * may also reach the tokens that do not see it.  With q_start (prompts) a plan with
+ * may also reach the tokens that do not see it.  o, lse and the workspace
+ * overlap none of the inputs.  With q_start (prompts) a plan with
  * TPL_FP32_WEIGHTS is TPL_EUNSUPPORTED, as in prefill.  The same inputs give
  * the same bits. */
 int tpl_paged_attn(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,

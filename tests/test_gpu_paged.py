@@ -393,3 +393,99 @@ def test_numbers_outside_their_range_are_reported(gpu):
             changed = (c.k != old).permute(1, 3, 0, 2, 4).flatten(2).any(-1).sum()
             assert int(changed) <= sum(c.news)
             assert plan.last_device_error() == tpl.TPL_OK
+
+
+# ---- the ends of the ranges -------------------------------------------------------
+
+def moved_to_the_end(c, n_pages):
+    """The same batch in a pool of n_pages pages, its pages the last ones."""
+    shift = n_pages - c.n_pages
+    for name in ("k", "v"):
+        small = getattr(c, name)
+        big = torch.empty((small.shape[0], n_pages, *small.shape[2:]), dtype=small.dtype, device=small.device)
+        big[:, shift:] = small
+        setattr(c, name, big)
+    c.pages = [[p + shift if p < c.n_pages else p for p in row] for row in c.pages]
+    c.table += torch.where(c.table < c.n_pages, shift, 0).to(torch.int32) * (c.table >= 0)
+    c.n_pages = n_pages
+    return c
+
+
+@pytest.mark.parametrize("kind", ["tokens", "prompts", "shared"])
+def test_offsets_beyond_32_bits(gpu, kind):
+    """20.5 million rows of the pool: 2.6e9 values, 5.2 GB each for k and v."""
+    plan = plan_of(16, 2, 2)
+    news = [40, 3] if kind == "prompts" else None
+    c = moved_to_the_end(Case(gpu, 16, 2, 2, 256, [1000, 513], news, shared=256 if kind == "shared" else 0, seed=3), 40000)
+    k = torch.randn((c.tokens, 2, D), device=gpu)
+    v = torch.randn((c.tokens, 2, D), device=gpu)
+    plan.paged_append(c.kv(plan), c.batch(plan), k, v)
+    for b, r, pos in c.rows():
+        want = v[r].to(torch.bfloat16)
+        assert torch.equal(c.v[:, c.pages[b][pos // 256], :, pos % 256].flatten(0, 1), want)
+    if kind == "shared":
+        o, lse = outputs(c)
+        plan.paged_attn_shared(c.kv(plan), c.batch(plan), 256, c.q, o, workspace(plan, c), lse=lse)
+        assert plan.last_device_error() == tpl.TPL_OK
+    else:
+        o, lse = run_attn(plan, c)
+    check(c, o, lse, 0, 0, TOKEN_Q, TOKEN_Q if kind == "tokens" else PROMPT_P)
+
+
+@pytest.mark.parametrize("kind", ["tokens", "prompts", "shared"])
+def test_a_batch_that_sees_nothing(gpu, kind):
+    plan = plan_of(16, 8, 1)
+    n = 1024
+    c = Case(gpu, 16, 8, 1, 16, [0] * n, [1] * n if kind == "prompts" else None, shared=32 if kind == "shared" else 0, seed=3,
+             fill=float("nan"))
+    o, lse = outputs(c)
+    if kind == "shared":
+        plan.paged_attn_shared(c.kv(plan), c.batch(plan), 32, c.q, o, workspace(plan, c), lse=lse)
+    else:
+        plan.paged_attn(c.kv(plan), c.batch(plan), c.q, o, workspace(plan, c), lse=lse)
+    assert (o == 0).all() and (lse == -float("inf")).all() and plan.last_device_error() == tpl.TPL_OK
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_many_sequences_of_any_length(gpu, seed):
+    rnd = random.Random(seed)
+    nkv = rnd.choice([1, 2, 4, 8])
+    nq = nkv * rnd.choice([1, 2, 3, 5, 7, 8, 9, 11, 16])
+    t = rnd.choice([x for x in (1, 2, 4) if nkv % x == 0])
+    page = rnd.choice([16, 32, 64, 128, 256])
+    n = rnd.choice([1, 2, 33, 147, 1024]) if seed else 1024
+    top = max(3, 40000 // n)
+    kv_len = [rnd.choice([0, 1, rnd.randrange(top), rnd.randrange(top)]) for _ in range(n)]
+    kind = seed % 3
+    news = [rnd.randrange(0, 1 + min(x, 2 + 600 // n)) if rnd.random() < 0.9 else 0 for x in kv_len] if kind == 1 else None
+    window, sinks = (rnd.choice([0, 1, 63, 64, 65, 300]), rnd.choice([0, 1, 64, 200])) if kind < 2 else (0, 0)
+    shared = page * rnd.randrange(1, 9) if kind == 2 else 0
+    plan = plan_of(nq, nkv, t)
+    dtype = rnd.choice([torch.float32, torch.bfloat16])
+    c = Case(gpu, nq, nkv, t, page, kv_len, news, shared=shared, dtype=dtype, seed=seed, rows_behind=1 if news else 0,
+             fill=float("nan"))
+    if kind == 2:
+        o, lse = outputs(c)
+        plan.paged_attn_shared(c.kv(plan), c.batch(plan), shared, c.q, o, workspace(plan, c), lse=lse)
+        assert plan.last_device_error() == tpl.TPL_OK
+    else:
+        o, lse = run_attn(plan, c, window, sinks)
+    check(c, o, lse, window, sinks, q_bits(c, kind == 0), TOKEN_Q if kind == 0 else PROMPT_P)
+
+
+def test_captured_before_any_eager_call(gpu):
+    """A graph whose first launches are the captured ones (its own process state aside)."""
+    plan = plan_of(20, 4, 4)
+    c = Case(gpu, 20, 4, 4, 64, [700, 65, 3], seed=9)
+    o, lse = outputs(c)
+    kv, batch, ws = c.kv(plan), c.batch(plan), workspace(plan, c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.paged_attn(kv, batch, c.q, o, ws, lse=lse)
+    for _ in range(3):
+        o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(c, o, lse, 0, 0, TOKEN_Q, TOKEN_Q)
+    assert plan.last_device_error() == tpl.TPL_OK
