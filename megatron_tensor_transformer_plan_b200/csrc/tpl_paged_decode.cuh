@@ -495,35 +495,49 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             w.j = (int)paged_div(rel, w.sp.nblk);
             pair_start += (int64_t)w.j * w.sp.nblk;
         }
-        // the queries of segment seg: rows of hi parts, then of lo parts
+        // The queries of the segments to come: loaded three segments ahead, stored (rows of hi
+        // parts, then of lo parts) two ahead, when the consumers are done with the buffer.
         ahead = w;
         int64_t ahead_at = pair_start;  // where its pair begins; at or behind u1: no such segment
         int staged = 0;
-        auto stage_q = [&]() {
-            if (ahead_at >= u1) return;
-            unsigned char *q = s_q + (staged & 1) * SM::Q;
+        bool held = false;
+        uint4 raw[2 * RPT][2];
+        auto load_q = [&]() {
+            held = ahead_at < u1;
+            if (!held) return;
 #pragma unroll
             for (int r = 0; r < 2 * RPT; ++r) {
                 const int hd = tid / 16 + 4 * r, ch = tid % 16;  // 8 dims
-                float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                raw[r][0] = raw[r][1] = make_uint4(0, 0, 0, 0);
                 if (hd < a.g) {
                     const int64_t off = ahead.b * a.q_ts + (ahead.j * a.g + hd) * a.q_hs + 8 * ch;
-                    if (a.q_f32) {
-                        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + off);
-                        const float4 x = p[0], y = p[1];
-                        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
-                    } else {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + off);
-                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[2 * e] = bf16lo(y[e]), f[2 * e + 1] = bf16hi(y[e]);
-                    }
+                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.q) + off * (a.q_f32 ? 4 : 2));
+                    raw[r][0] = p[0];
+                    if (a.q_f32) raw[r][1] = p[1];
                 }
+            }
+            ahead_at += ahead.sp.nblk;
+            if (ahead_at < u1) ahead.next(a, s_start, s_len);
+        };
+        auto store_q = [&]() {
+            if (!held) return;
+            unsigned char *q = s_q + (staged & 1) * SM::Q;
+#pragma unroll
+            for (int r = 0; r < 2 * RPT; ++r) {
+                const int hd = tid / 16 + 4 * r, ch = tid % 16;
                 uint32_t h[4], lo[4];
+                const uint32_t y[8] = {raw[r][0].x, raw[r][0].y, raw[r][0].z, raw[r][0].w,
+                                       raw[r][1].x, raw[r][1].y, raw[r][1].z, raw[r][1].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    h[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-                    lo[e] = pack_bf16x2(f[2 * e] - bf16lo(h[e]), f[2 * e + 1] - bf16hi(h[e]));
+                    if (a.q_f32) {
+                        const float f0 = __uint_as_float(y[2 * e]), f1 = __uint_as_float(y[2 * e + 1]);
+                        h[e] = pack_bf16x2(f0, f1);
+                        lo[e] = pack_bf16x2(f0 - bf16lo(h[e]), f1 - bf16hi(h[e]));
+                    } else {
+                        h[e] = y[e];
+                        lo[e] = 0u;
+                    }
                 }
                 const int at = (ch ^ (hd & 7)) << 4;
                 *reinterpret_cast<uint4 *>(q + hd * 256 + at) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -532,30 +546,38 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[staged & 1]);
             ++staged;
-            ahead_at += ahead.sp.nblk;
-            if (ahead_at < u1) ahead.next(a, s_start, s_len);
         };
-        stage_q();
-        stage_q();
+        load_q();
+        store_q();
+        load_q();
+        store_q();
+        load_q();
         for (int seg = 0; pair_start < u1; ++seg) {
             const int64_t pair_end = pair_start + w.sp.nblk;
             const int slot = seg % NB;
             const float *so = s_o + slot * (SM::STATE / 4), *sml = s_ml + slot * (SM::ML / 4);
             if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&st_full[slot], (unsigned)(seg / NB) & 1u));
-            stage_q();  // (into the buffer of this segment: every consumer is done with it)
-            if (tid < a.g) {
-                float M = -INFINITY, den = 0.f;
+            store_q();  // (into the buffer of this segment: every consumer is done with it)
+            load_q();
+            // weights of the eight states of a head: eight lanes side by side
 #pragma unroll
-                for (int x = 0; x < kAmWarps; ++x) M = fmaxf(M, sml[(x * GM + tid) * 2]);
+            for (int r = 0; r < RPT; ++r) {
+                const int x = tid & 7, hd = (tid >> 3) + 8 * r;
+                const float2 ml = hd < a.g ? *reinterpret_cast<const float2 *>(sml + (x * GM + hd) * 2) : make_float2(-INFINITY, 0.f);
+                float M = ml.x;
 #pragma unroll
-                for (int x = 0; x < kAmWarps; ++x) {
-                    const float2 ml = *reinterpret_cast<const float2 *>(sml + (x * GM + tid) * 2);
-                    const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-                    s_wt[x * GM + tid] = wt;
-                    den += wt * ml.y;
+                for (int k = 4; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+                const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                float den = wt * ml.y;
+#pragma unroll
+                for (int k = 4; k > 0; k >>= 1) den += __shfl_xor_sync(0xffffffffu, den, k);
+                if (hd < a.g) {
+                    s_wt[x * GM + hd] = wt;
+                    if (x == 0) {
+                        s_M[hd] = M;
+                        s_den[hd] = den;
+                    }
                 }
-                s_M[tid] = M;
-                s_den[tid] = den;
             }
             meet();
             const bool whole = pair_start >= u0 && pair_end <= u1;
