@@ -26,8 +26,11 @@
 // 16 they are two products.  tcgen05 would pad the g rows to 128.
 // At the end of a pair the eight warps leave their states in shared memory and
 // go on; two merging warps join them, write the result and bring the queries
-// of the pair after next, so that short sequences do not wait on each other's
-// ends (64 sequences of 130 to 512 keys behind a prefix: 72 us without them).
+// of later pairs, so that short sequences do not wait on each other's ends (the
+// keys of 64 sequences of 130 to 512 behind a prefix: 72 us before, 47 with
+// them).
+// Measured: 16 tokens at 8193 keys, 64/8 heads, 95 us (5.7 TB/s); 32 tokens with
+// a window of 4096 on pages of 16, 100 us (5.2 TB/s).
 //
 // A page none of whose keys is visible is not read, nor is its table entry;
 // keys that are not visible are masked by a select and their values replaced
