@@ -112,7 +112,7 @@ __device__ __forceinline__ PtItem pt_item(const PagedPromptArgs &a, int len, int
     x.ntok = min(2 * a.tb, count - t0);
     if (a.shared > 0) {
         x.p0 = a.shared;
-        x.len = a.shared;
+        x.len = min(a.shared, len);
         x.lo = x.sk = x.nst = x.ft = 0;
         x.ntk = (a.shared + kPtKeys - 1) / kPtKeys;
         return x;
@@ -128,11 +128,24 @@ __device__ __forceinline__ PtItem pt_item(const PagedPromptArgs &a, int len, int
     return x;
 }
 
+// Keys of the longest sequence behind a prefix, by the whole warp; `len`: lane's sequence's.
+// A prefix that no sequence fills is read, and its values are taken, up to there: what lies
+// behind it may be anything, and 0 * NaN is NaN.  The two warps that need it (the loads and
+// the check of the values) ask; the softmax masks by each row's own length.  One sequence
+// that goes on behind the prefix is enough to know, and is most often among the first 32.
+__device__ __forceinline__ int pt_longest(const PagedPromptArgs &a, int lane, int len) {
+    int top = paged_len_ok(a.v, len);
+    if (__any_sync(0xffffffffu, top >= a.shared)) return a.shared;
+#pragma unroll 1
+    for (int b = lane + 32; b < a.v.n_seqs; b += 32) top = max(top, paged_len(a.v, b));
+    return __reduce_max_sync(0xffffffffu, top);
+}
+
 // Walks a CTA's segments in order; every role walks on its own.
 struct PtWalk {
     int64_t u, u1;
     int j, b, it;        // kv head, sequence, item of the sequence
-    int start, count, len;  // its tokens and keys
+    int start, count, len;  // its tokens and keys (a prefix: see pt_longest)
     int done;            // key tiles of the item before u
     int idx;             // items before this one, over all kv heads (prefix mode)
     PtItem x;
@@ -148,7 +161,6 @@ struct PtWalk {
         if (a.shared > 0) {
             start = 0;
             count = a.v.n_tokens;
-            len = 0;
         } else {
             paged_seq(a.v, b, start, count, len);
         }
@@ -306,7 +318,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
 
     // ---- this CTA's range of the key tiles ----
     int64_t U1;  // key tiles of one kv head
+    int lane_len = 0;  // a prefix: keys of sequence `lane`
     if (a.shared > 0) {
+        if ((warp == 0 || warp == 2) && lane < a.v.n_seqs) lane_len = a.v.kv_len[lane];
         U1 = (int64_t)pt_items(a, a.v.n_tokens) * ((a.shared + kPtKeys - 1) / kPtKeys);
     } else {
         // the sequences' items, tokens and keys; then each thread sums a run of items
@@ -422,6 +436,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
             w.j = w.idx / items;
             w.it = w.idx - w.j * items;
             w.b = 0;
+            w.len = warp == 0 || warp == 2 ? pt_longest(a, lane, lane_len) : a.shared;
             w.tokens(a);
         } else {
             w.j = s_where[0];
