@@ -43,6 +43,13 @@ __device__ __forceinline__ int paged_len_ok(const PagedView &v, int len) {
 // Keys of sequence b.
 __device__ __forceinline__ int paged_len(const PagedView &v, int b) { return paged_len_ok(v, v.kv_len[b]); }
 
+// Whether s .. e - 1 are rows of a sequence.
+__device__ __forceinline__ bool paged_starts_ok(const PagedView &v, int s, int e) {
+    if (s >= 0 && e >= s && e <= v.n_tokens) return true;
+    record_error(kErrPaged);
+    return false;
+}
+
 // First token row, token count and keys of sequence b (its loads go out together).
 __device__ __forceinline__ void paged_seq(const PagedView &v, int b, int &start, int &count, int &len) {
     int s = b, e = b + 1;
@@ -53,10 +60,7 @@ __device__ __forceinline__ void paged_seq(const PagedView &v, int b, int &start,
     len = paged_len(v, b);
     start = s;
     count = e - s;
-    if (s < 0 || e < s || e > v.n_tokens) {
-        record_error(kErrPaged);
-        start = count = 0;
-    }
+    if (!paged_starts_ok(v, s, e)) start = count = 0;
 }
 
 // The pool row (128 values) of page entry `entry` of sequence b for global kv
@@ -201,8 +205,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     // the tokens' sequences: every thread looks at some of them
     if (a.v.q_start) {
         for (int b = threadIdx.x; b < a.v.n_seqs; b += kAppendThreads) {
-            const int first = max(a.v.q_start[b], tok0), end = min(a.v.q_start[b + 1], tok0 + ntok);
-            for (int x = first; x < end; ++x) atomicMax(&s_seq[x - tok0], b);
+            const int s = a.v.q_start[b], e = a.v.q_start[b + 1];
+            if (!paged_starts_ok(a.v, s, e)) continue;  // (reported though none of its rows may be this CTA's)
+            for (int x = max(s, tok0); x < min(e, tok0 + ntok); ++x) atomicMax(&s_seq[x - tok0], b);
         }
     } else if (threadIdx.x < ntok) {
         s_seq[threadIdx.x] = tok0 + threadIdx.x;

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from megatron_tensor_transformer_plan_b200 import tpl
-from tests.paged_util import Case, check, outputs, plan_of
+from tests.paged_util import D, Case, check, outputs, plan_of
 from tests.test_gpu_paged import PROMPT_P, q_bits, workspace
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +50,47 @@ def test_a_prefix_that_no_sequence_fills(gpu, p, dtype, stale):
     c.table[:, (top + page - 1) // page:] = -3
     o, lse = run_shared(plan, c, shared)
     check(c, o, lse, 0, 0, q_bits(c, False), PROMPT_P)
+
+
+# ---- starts that are out of range ------------------------------------------------
+
+STARTS = [
+    # q_start with n_tokens = 60, the rows that some sequence validly has
+    ([0, 50, 20, 60], [(0, 0, 20), (2, 20, 60)]),       # (rows 20 .. 49 lie in two sequences: either may lack them)
+    ([70, 75], []),
+    ([-5, -2], []),
+    ([0, 10, 61, 62, 70], [(0, 0, 10)]),
+    ([60, 65], []),
+    ([-1, 10, 30], [(1, 10, 30)]),
+    ([0, 10, 10, 5], [(0, 0, 10)]),
+]
+
+
+@pytest.mark.parametrize("p", STARTS)
+def test_append_reports_starts_out_of_range(gpu, p):
+    starts, valid = p
+    plan = plan_of(16, 8, 2, rope=False)
+    n, tokens, page = len(starts) - 1, 60, 16
+    c = Case(gpu, 16, 8, 2, page, [100] * n, [0] * n, seed=2)
+    q_start = torch.tensor(starts, dtype=torch.int32, device=gpu)
+    batch = plan.paged_batch(c.table, c.lens, q_start, tokens)
+    k, v = (torch.randn((tokens, 8, D), device=gpu) for _ in "kv")
+    want = c.k.clone(), c.v.clone()
+    loose = torch.zeros((c.n_pages, page), dtype=torch.bool, device=gpu)  # slots that may or may not be written
+    for b, first, end in valid:
+        for r in range(first, end):
+            pos = 100 - starts[b + 1] + r
+            for pool, x in zip(want, (k, v)):
+                pool[:, c.pages[b][pos // page], :, pos % page] = x[r].to(torch.bfloat16).unflatten(0, (2, 4))
+    for b in range(n):
+        if 0 <= starts[b] <= starts[b + 1] <= tokens:
+            for r in range(starts[b], starts[b + 1]):
+                if sum(starts[x] <= r < starts[x + 1] <= tokens and starts[x] >= 0 for x in range(n)) > 1:
+                    pos = 100 - starts[b + 1] + r
+                    loose[c.pages[b][pos // page], pos % page] = True
+    plan.paged_append(c.kv(plan), batch, k, v)
+    assert plan.last_device_error() == tpl.TPL_EDEVICE
+    for pool, w in zip((c.k, c.v), want):
+        same = (pool == w).permute(1, 3, 0, 2, 4).flatten(2).all(-1)
+        assert (same | loose).all()
+    assert plan.last_device_error() == tpl.TPL_OK
