@@ -435,7 +435,9 @@ int tpl_paged_append(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_pag
  * tokens that stay visible behind a window).  A page none of whose keys is
  * seen is not read, nor is its table entry.  o: [n_tokens][n_q * d], the activation
  * type; lse: fp32 [n_tokens][n_q] or NULL, the natural logarithm of the
- * softmax denominator.  A token that sees no key gets o = 0, lse = -inf.
+ * softmax denominator.  A token that sees no key gets o = 0, lse = -inf, and so
+ * does one whose every logit falls below fp32's range; such a key beside others
+ * weighs nothing.  (An infinity in q, or in a key that is seen, may give NaN.)
  * Logits are q.k / sqrt(d); q is TPL_F32 or TPL_BF16 (fp32 queries cost the
  * prompts a second product).  What lies in slots that no token of the call sees
  * has no effect, whatever it is; a NaN or an infinity among the values of a key

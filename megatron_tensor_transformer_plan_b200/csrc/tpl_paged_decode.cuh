@@ -405,8 +405,9 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                         float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        // one of the 16 keys is visible, so mx is a logit.  Raise the
-                        // running maximum only past the margin: until then p <= 2^kAmLazy.
+                        // one of the 16 keys is visible, so mx is a logit (which may have
+                        // fallen below fp32's range).  Raise the running maximum only past
+                        // the margin: until then p <= 2^kAmLazy.
                         if (mx > m[r] + kAmLazy) {
                             const float alpha = exp2f(m[r] - mx);  // 0 on the first step (m = -inf)
                             m[r] = mx;
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                                 }
                             }
                         }
-                        const float p0 = ex2(x0 - m[r]), p1 = ex2(x1 - m[r]), p2 = ex2(x2 - m[r]),
-                                    p3 = ex2(x3 - m[r]);
+                        const float sub = m[r] == -INFINITY ? 0.f : m[r];  // only logits of -inf so far: 2^-inf each
+                        const float p0 = ex2(x0 - sub), p1 = ex2(x1 - sub), p2 = ex2(x2 - sub), p3 = ex2(x3 - sub);
                         l[r] += (p0 + p1) + (p2 + p3);
                         ph[r][0] = pack_bf16x2(p0, p1);
                         ph[r][1] = pack_bf16x2(p2, p3);
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                     reinterpret_cast<float4 *>(a.own_o + row * D)[lane] = num;
                     if (lane == 0) *reinterpret_cast<float2 *>(a.own_ml + row * 2) = make_float2(M, den);
                 } else {
-                    const float inv = 1.f / den;
+                    const float inv = den != 0.f ? 1.f / den : 0.f;  // 0: only logits of -inf
                     if (a.o_f32)
                         reinterpret_cast<float4 *>(static_cast<float *>(a.o) + row * D)[lane] =
                             make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);

@@ -1,10 +1,12 @@
 """What the paged-cache calls do at the edges of what a batch may hold."""
+import math
+
 import pytest
 import torch
 
 from megatron_tensor_transformer_plan_b200 import tpl
 from tests.paged_util import D, Case, check, outputs, plan_of
-from tests.test_gpu_paged import PROMPT_P, q_bits, workspace
+from tests.test_gpu_paged import PROMPT_P, TOKEN_Q, q_bits, run_attn, workspace
 
 pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
@@ -94,3 +96,55 @@ def test_append_reports_starts_out_of_range(gpu, p):
         same = (pool == w).permute(1, 3, 0, 2, 4).flatten(2).all(-1)
         assert (same | loose).all()
     assert plan.last_device_error() == tpl.TPL_OK
+
+
+# ---- logits beyond fp32 -----------------------------------------------------------
+
+def overflowing(gpu, nq, nkv, kv_len, low, dtype, news=None, shared=0):
+    """Every q is 2^66; the first `low` keys are -2^66 (their logits fall below
+    fp32's range, a weight of 0), the others give logits of deviation 1."""
+    c = Case(gpu, nq, nkv, 1, 64, kv_len, news, shared=shared, dtype=dtype, seed=3)
+    c.q.fill_(2.0 ** 66)
+    c.k.mul_(2.0 ** -66)
+    for b, n in enumerate(kv_len):
+        for key in range(min(low, n)):
+            c.k[:, c.pages[b][key // 64], :, key % 64] = -2.0 ** 66
+    return c
+
+
+@pytest.mark.parametrize("kind", ["tokens", "prompts", "shared"])
+@pytest.mark.parametrize("heads", [(16, 8), (32, 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low", [20, 64, 200])
+def test_logits_below_the_range(gpu, kind, heads, dtype, low):
+    """A key whose logit overflows to -inf has no weight; a token that sees
+    only such keys gets what one that sees no key gets."""
+    nq, nkv = heads
+    kv_len = [300, 1300, 40, 150]
+    news = [7, 30, 40, 1] if kind == "prompts" else None
+    shared = 128 if kind == "shared" else 0
+    if shared:
+        kv_len = [300, 1300, 140, 129]
+    plan = plan_of(nq, nkv, 1)
+    c = overflowing(gpu, nq, nkv, kv_len, low, dtype, news, shared)
+    o, lse = run_shared(plan, c, shared) if shared else run_attn(plan, c)
+    o = o.view(-1, nq, D).double()
+    g = nq // nkv
+    for b, row, pos in c.rows():
+        if pos < low:
+            assert (o[row] == 0).all() and (lse[row] == -INF).all(), (b, pos)
+            continue
+        K, V = c.keys(b, c.k)[low:pos + 1], c.keys(b, c.v)[low:pos + 1]
+        q = c.q[row].double().unflatten(0, (nkv, g))
+        s = torch.einsum("jgd,kjd->jgk", q, K) / math.sqrt(D)
+        p = torch.softmax(s, -1)
+        ref, mag = torch.einsum("jgk,kjd->jgd", p, V).flatten(0, 1), torch.einsum("jgk,kjd->jgd", p, V.abs()).flatten(0, 1)
+        # q is exact; a logit adds 128 products in fp32, a weight rounds to p_bits, the sums add in fp32
+        E = torch.einsum("jgd,kjd->jgk", q.abs(), K.abs()).amax(-1).flatten()[:, None] / math.sqrt(D) * 128 * 2.0 ** -24
+        n = pos + 1 - low
+        p_bits = TOKEN_Q if kind == "tokens" else PROMPT_P
+        rel = 2 * E + 2.0 ** -p_bits + (n + 64) * 2.0 ** -24 + 2.0 ** -20
+        assert ((o[row] - ref).abs() <= 2 * rel * mag + 2.0 ** -8 * ref.abs()).all(), (b, pos)
+        z = torch.logsumexp(s, -1).flatten()
+        lt = E[:, 0] + (n + 64) * 2.0 ** -24 + 2.0 ** -20 * (1 + z.abs())
+        assert ((lse[row].double() - z).abs() <= lt).all(), (b, pos)
