@@ -922,7 +922,7 @@ __device__ __forceinline__ void paged_join_row(int lane, int n, const float *par
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
     auto add = [&](float wt, float l, const float4 *p) {
-        if (wt == 0.f) return;  // nothing seen: the part's outputs may be anything
+        if (l == 0.f) return;  // nothing seen: the part's outputs may be anything (NaN keys: l is NaN)
         const float4 y = __ldcg(p + lane);
         num.x += wt * y.x;
         num.y += wt * y.y;

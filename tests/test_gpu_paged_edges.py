@@ -148,3 +148,23 @@ def test_logits_below_the_range(gpu, kind, heads, dtype, low):
         z = torch.logsumexp(s, -1).flatten()
         lt = E[:, 0] + (n + 64) * 2.0 ** -24 + 2.0 ** -20 * (1 + z.abs())
         assert ((lse[row].double() - z).abs() <= lt).all(), (b, pos)
+
+
+# ---- keys that are no numbers -------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["tokens", "prompts", "shared own", "shared prefix"])
+def test_a_seen_key_that_is_no_number_is_seen(gpu, kind):
+    """NaN among the keys that a token sees gives it NaN, also where all keys
+    of one part of the work are NaN; other sequences do not notice."""
+    news = [3, 2, 5] if kind == "prompts" else None
+    shared = 1024 if kind.startswith("shared") else 0
+    plan = plan_of(16, 8, 1)
+    c = Case(gpu, 16, 8, 1, 64, [1025, 1100, 1025 + 64], news, shared=shared, seed=4)
+    for key in range(1024, 1025) if kind == "shared own" else range(256, 512):
+        c.k[:, c.pages[0][key // 64], :, key % 64] = NAN
+    o, lse = run_shared(plan, c, shared) if shared else run_attn(plan, c)
+    o = o.view(-1, 16, D)
+    for b, row, _ in c.rows():
+        hit = b == 0 or kind == "shared prefix"
+        assert torch.isnan(o[row]).all() == hit and torch.isnan(lse[row]).all() == hit
+        assert hit or (torch.isfinite(o[row]).all() and torch.isfinite(lse[row]).all())
