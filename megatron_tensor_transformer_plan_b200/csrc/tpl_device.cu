@@ -44,7 +44,9 @@ namespace {
 
 // Launch with programmatic dependent launch enabled: the kernel may start
 // while the previous kernel on the stream drains; every kernel here waits
-// (griddepcontrol.wait) before touching data a previous kernel wrote.
+// (griddepcontrol.wait) before touching data a previous kernel wrote, but for
+// paged_decode_kernel behind a shared prefix (pdl_pass_on says how that is sound).
+// All kernels wait before they end, so a wait covers everything earlier.
 template <typename... KA, typename... A>
 cudaError_t launch_pdl(void (*kern)(KA...), dim3 grid, int block, size_t smem, cudaStream_t st, A &&...args) {
     cudaLaunchConfig_t cfg = {};

@@ -136,6 +136,7 @@ int prefill_ws_layout(const tpl_plan *p, int64_t T, PrefillWs *w);
 constexpr int kPagedMaxSeqs = 1024;       // sequences per call
 constexpr int kPagedMaxTokens = 1 << 22;  // rows of q per call
 constexpr int kPagedMaxCtas = 160;        // CTAs of one paged attention launch at most
+constexpr int kTicketPagedReady = kTicketAttn + kPagedMaxCtas;  // behind the paged tickets: the word of pdl_pass_on
 
 // Workspace of the paged attention calls (byte offsets).
 struct PagedWs {

@@ -91,8 +91,10 @@ struct PagedDecodeArgs {
     float *lse;              // [n_seqs][nq] or NULL
     float *own_o;            // when set (a shared prefix): unnormalised fp32 outputs [n_seqs][nq][128]
     float *own_ml;           // and (max, sum) [n_seqs][nq][2] instead of o and lse.  The kernel before this
-                             // one is then the prefix's: it has waited for all that came before, and nothing
-                             // here needs it, so this one starts at once and waits for it at its end.
+                             // one is then the prefix's: it has waited for all that came before and passes
+                             // that on by `ready`; nothing here needs it, so this one starts at once and waits
+                             // for it at its end.
+    const unsigned *ready;
 };
 
 // What one sequence's token sees, in keys and in blocks.
@@ -145,6 +147,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     unsigned char *sm = pd_raw;
     if (smem_u32(sm) & 1023u) {  // (the whole grid: the swizzled stages need 1 KB alignment)
         if (threadIdx.x == 0) record_error(8u);
+        pdl_wait();
         return;
     }
     unsigned char *s_q = sm + NS * kPdStage;                                   // [2][hi, lo][GM][256 B], swizzled
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         s_flag[2] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (!a.own_o) pdl_wait();
+    if (!a.own_o || !pdl_passed_on(a.ready)) pdl_wait();
     pdl_trigger();
 
     // ---- prefix sums of the sequences' blocks (all kv heads) ----

@@ -190,6 +190,7 @@ int paged_decode(const PagedCall &c, int window, int sinks, int base, bool own) 
     if (own) {
         a.own_o = reinterpret_cast<float *>(c.ws + c.L.own_o);
         a.own_ml = reinterpret_cast<float *>(c.ws + c.L.own_ml);
+        a.ready = reinterpret_cast<const unsigned *>(c.ws + c.L.tickets) + kTicketPagedReady;
     }
     const int grid = std::min(sms, kPagedMaxCtas);
     return a.g <= 8 ? paged_decode_go<8>(a, grid, c.st) : paged_decode_go<16>(a, grid, c.st);
@@ -255,6 +256,7 @@ int paged_shared(const PagedCall &c, int shared) {
     int rc = paged_prompt_args(c, &a, &grid);
     if (rc != TPL_OK) return rc;
     a.shared = shared;
+    a.ready = reinterpret_cast<unsigned *>(c.ws + c.L.tickets) + kTicketPagedReady;
     // The CTAs: as many per item as there are, so that no CTA has parts of two (64 sequences,
     // 8192 keys: 16 items, 144 CTAs rather than 148), when there are more CTAs than items.
     const int64_t items = (int64_t)((c.v.n_tokens + 2 * a.tb - 1) / (2 * a.tb)) * c.v.nkv;

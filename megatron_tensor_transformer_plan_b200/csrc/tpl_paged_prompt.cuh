@@ -86,6 +86,7 @@ struct PagedPromptArgs {
     float *part_o, *part_ml;
     int part_rows;           // rows per slot
     int G;                   // CTAs that take part (0: decided at the device)
+    unsigned *ready;         // prefix: set once all that came before this kernel is there (pdl_pass_on)
     int4 *cut;               // [grid] prompts: {first token, row tokens, kv head, parts} of the item CTA c is the first of
 };
 
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     unsigned char *sm = pt_raw;
     if (smem_u32(sm) & 1023u) {  // (the whole grid: the swizzled tiles need 1 KB alignment)
         if (threadIdx.x == 0) record_error(8u);
+        pdl_wait();
         return;
     }
     unsigned char *s_q = sm;              // [tile][part][half][128 rows][128 B]
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_prompt_kernel(const __gri
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
+    if (a.ready && cta == 0 && threadIdx.x == 0) pdl_pass_on(a.ready);
     pdl_trigger();
 
     // ---- this CTA's range of the key tiles ----
@@ -976,6 +979,7 @@ __global__ void __launch_bounds__(kPtJoinThreads) paged_shared_join_kernel(const
     pdl_wait();
     pdl_trigger();
     const PagedPromptArgs &a = g.p;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * kPtJoinRows + warp;
     if (row >= (int64_t)a.v.n_tokens * a.nq) return;

@@ -168,3 +168,37 @@ def test_a_seen_key_that_is_no_number_is_seen(gpu, kind):
         hit = b == 0 or kind == "shared prefix"
         assert torch.isnan(o[row]).all() == hit and torch.isnan(lse[row]).all() == hit
         assert hit or (torch.isfinite(o[row]).all() and torch.isfinite(lse[row]).all())
+
+
+# ---- calls that follow each other ---------------------------------------------------
+
+def test_own_keys_appended_by_the_call_before(gpu):
+    """Behind a shared prefix the kernel of the sequences' own keys starts under
+    the prefix's; it has to see what an append just before wrote.  Step after step
+    with other keys and queries, against the same steps one kernel at a time."""
+    plan = plan_of(32, 8, 2)
+    shared, own, steps = 256, 700, 40
+    c = Case(gpu, 32, 8, 2, 64, [shared + own] * 4, shared=shared, seed=6)
+    kv, batch, ws = c.kv(plan), c.batch(plan), workspace(plan, c)
+    start = torch.arange(5, dtype=torch.int32, device=gpu) * own
+    prompts = plan.paged_batch(c.table, c.lens, start, 4 * own)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(1)
+    k, v = (torch.randn((4, 4 * own, 8, D), generator=g, device=gpu) for _ in "kv")
+    q = torch.randn((4, 4, 32, D), generator=g, device=gpu)
+
+    def step(s, wait):
+        o, lse = outputs(c)
+        plan.paged_append(kv, prompts, k[s % 4], v[(s + s // 4) % 4])
+        if wait:
+            torch.cuda.synchronize()
+        plan.paged_attn_shared(kv, batch, shared, q[(s + s // 7) % 4], o, ws, lse=lse)
+        if wait:
+            torch.cuda.synchronize()
+        return o, lse
+
+    got = [step(s, False) for s in range(steps)]
+    for s in range(steps):
+        o, lse = step(s, True)
+        assert torch.equal(o, got[s][0]) and torch.equal(lse, got[s][1]), s
+    assert plan.last_device_error() == tpl.TPL_OK
