@@ -1,5 +1,8 @@
 """What the paged-cache calls do at the edges of what a batch may hold."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -202,3 +205,121 @@ def test_own_keys_appended_by_the_call_before(gpu):
         o, lse = step(s, True)
         assert torch.equal(o, got[s][0]) and torch.equal(lse, got[s][1]), s
     assert plan.last_device_error() == tpl.TPL_OK
+
+
+def test_first_calls_of_a_process_are_captured(gpu):
+    """Append, tokens, prompts and a shared prefix, captured in a process that has
+    launched none of them before."""
+    code = """
+import torch
+from megatron_tensor_transformer_plan_b200 import tpl
+from tests.paged_util import D, Case, check, outputs, plan_of
+gpu = torch.device("cuda:0")
+plan = plan_of(20, 4, 4, rope=False)
+runs = []
+for kind in ("tokens", "prompts", "shared"):
+    c = Case(gpu, 20, 4, 4, 64, [700, 165, 130], [40, 3, 9] if kind == "prompts" else None,
+             shared=128 if kind == "shared" else 0, seed=9)
+    k, v = (torch.randn((c.tokens, 4, D), device=gpu) for _ in "kv")
+    runs.append((kind, c, k, v, outputs(c), c.kv(plan), c.batch(plan), plan.paged_workspace(3, c.tokens)))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for kind, c, k, v, (o, lse), kv, batch, ws in runs:
+        plan.paged_append(kv, batch, k, v)
+        if kind == "shared":
+            plan.paged_attn_shared(kv, batch, 128, c.q, o, ws, lse=lse)
+        else:
+            plan.paged_attn(kv, batch, c.q, o, ws, lse=lse)
+for _ in range(3):
+    for r in runs:
+        r[4][0].fill_(float("nan")), r[4][1].fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert plan.last_device_error() == tpl.TPL_OK
+    for kind, c, k, v, (o, lse), *_ in runs:
+        check(c, o, lse, 0, 0, 16, 16 if kind == "tokens" else 8)
+print("captured first: ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first: ok" in r.stdout, r.stdout + r.stderr
+
+
+# ---- plans with fp32 outputs ----------------------------------------------------------
+
+def test_fp32_outputs_are_closer_than_bf16(gpu):
+    """Few keys and small queries, so that the bound is far below a bf16 step."""
+    plan = plan_of(24, 8, 2, f32=True)
+    c = Case(gpu, 24, 8, 2, 32, [7, 1, 3, 30, 0], seed=5, q_scale=0.1)
+    o, lse = run_attn(plan, c, dtype=torch.float32)
+    ref, ref_lse, tol, ltol = c.expected(0, 0, TOKEN_Q, TOKEN_Q)
+    tol = tol - 2.0 ** -8 * ref.abs() + 2.0 ** -24 * ref.abs()  # fp32 in place of bf16 outputs
+    live = slice(0, 4)
+    o = o.view(5, 24, D).double()
+    assert ((o - ref).abs() <= tol).all()
+    assert ((lse.double() - ref_lse).abs()[live] <= ltol[live]).all() and (lse[4] == -INF).all()
+    rounded = ref.to(torch.bfloat16).double()
+    assert ((rounded - ref).abs() > tol)[live].double().mean() > 0.5  # (bf16 outputs would not pass)
+
+
+# ---- numbers outside their range: the others' results -----------------------------------
+
+@pytest.mark.parametrize("kind, bad", [(kind, bad) for kind in ("tokens", "prompts", "shared")
+                                       for bad in ("page", "page below", "length", "length below")] + [("prompts", "start")])
+def test_the_other_sequences_of_a_bad_one(gpu, kind, bad):
+    """Every other sequence is right, and an append writes its slots and no others."""
+    news = [5, 6, 7] if kind == "prompts" else None
+    shared = 64 if kind == "shared" else 0
+    plan = plan_of(32, 8, 2, rope=False)
+    c = Case(gpu, 32, 8, 2, 64, [300, 400, 500], news, shared=shared, seed=1)
+    wrong = 1
+    if bad.startswith("page"):
+        c.table[1, 6] = -1 if bad == "page below" else c.n_pages
+    elif bad.startswith("length"):
+        c.lens[1] = -9 if bad == "length below" else c.table.shape[1] * 64 + 1
+    else:
+        c.q_start[3], wrong = c.tokens + 1, 2
+    o, lse = outputs(c)
+    kv, batch, ws = c.kv(plan), c.batch(plan), workspace(plan, c)
+    if kind == "shared":
+        plan.paged_attn_shared(kv, batch, shared, c.q, o, ws, lse=lse)
+    else:
+        plan.paged_attn(kv, batch, c.q, o, ws, lse=lse)
+    assert plan.last_device_error() == tpl.TPL_EDEVICE
+    ref, ref_lse, tol, ltol = c.expected(0, 0, TOKEN_Q, TOKEN_Q if kind == "tokens" else PROMPT_P)
+    rows = [r for b, r, _ in c.rows() if b != wrong]
+    assert ((o.view(-1, 32, D).double() - ref).abs() <= tol)[rows].all()
+    assert ((lse.double() - ref_lse).abs() <= ltol)[rows].all()
+    k, v = (torch.randn((c.tokens, 8, D), device=gpu) for _ in "kv")
+    want = c.k.clone(), c.v.clone()
+    for b, r, pos in c.rows():
+        if b != wrong:
+            for pool, x in zip(want, (k, v)):
+                pool[:, c.pages[b][pos // 64], :, pos % 64] = x[r].to(torch.bfloat16).unflatten(0, (2, 4))
+    plan.paged_append(kv, batch, k, v)
+    assert plan.last_device_error() == tpl.TPL_EDEVICE
+    assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
+    assert plan.last_device_error() == tpl.TPL_OK
+
+
+# ---- padding and full tables --------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["tokens", "prompts", "shared"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_padded_rows_hold_anything(gpu, kind, dtype):
+    """Queries of inactive tokens and of rows that no sequence has may be NaN; the
+    longest sequence fills its row of the table to the last slot."""
+    news = [200, 5, 3, 4] if kind == "prompts" else None
+    shared = 128 if kind == "shared" else 0
+    plan = plan_of(16, 8, 2)
+    c = Case(gpu, 16, 8, 2, 32, [150, 0, 512, 3], news, shared=shared, dtype=dtype, seed=8, spare_entries=0,
+             rows_before=2 if news else 0, rows_behind=70 if news else 0, fill=NAN)
+    assert c.table.shape[1] * 32 == 512
+    idle = torch.ones(c.tokens, dtype=torch.bool, device=gpu)
+    idle[[r for _, r, pos in c.rows() if pos >= 0]] = False
+    q = c.q.clone()
+    c.q[idle] = NAN
+    o, lse = run_shared(plan, c, shared) if shared else run_attn(plan, c)
+    c.q = q
+    check(c, o, lse, 0, 0, q_bits(c, kind == "tokens"), TOKEN_Q if kind == "tokens" else PROMPT_P)
