@@ -978,47 +978,6 @@ int tpl_prefill_chunk(tpl_plan *p, const void *packed, const tpl_kv *kv, const v
                          L, reduce_mode, static_cast<cudaStream_t>(stream));
 }
 
-int tpl_paged_append(const tpl_plan *p, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,
-                     const tpl_heads *q_out, const tpl_heads *k, const tpl_heads *v, tpl_stream stream) {
-    PagedView view;
-    int rc = paged_view(p, kv, batch, &view);
-    if (rc != TPL_OK || view.n_tokens == 0) return rc;
-    if (!q != !q_out || (rc = check_heads(k)) != TPL_OK || (rc = check_heads(v)) != TPL_OK || v->type != k->type)
-        return TPL_EINVAL;
-    if (q && ((rc = check_heads(q)) != TPL_OK || (rc = check_out_heads(q_out, q, p->d.n_q_heads, view.n_tokens)) != TPL_OK ||
-              q->type != k->type))
-        return TPL_EINVAL;
-    return paged_append(p, kv, view, q, q_out, k, v, static_cast<cudaStream_t>(stream));
-}
-
-int tpl_paged_attn(const tpl_plan *p, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,
-                   int32_t window, int32_t sinks, void *o, float *lse, void *ws, size_t ws_bytes, tpl_stream stream) {
-    PagedView view;
-    int rc = paged_view(p, kv, batch, &view);
-    if (rc != TPL_OK) return rc;
-    if (window < 0 || sinks < 0) return TPL_EINVAL;
-    if (view.q_start && p->f32) return TPL_EUNSUPPORTED;
-    if (view.n_tokens == 0) return TPL_OK;
-    PagedCall c;
-    if ((rc = paged_call(p, kv, view, q, o, lse, ws, ws_bytes, stream, &c)) != TPL_OK) return rc;
-    return view.q_start ? paged_prompts(c, window, sinks) : paged_decode(c, window, sinks, 0, false);
-}
-
-int tpl_paged_attn_shared(const tpl_plan *p, const tpl_paged_kv *kv, const tpl_paged_batch *batch,
-                          int64_t shared_len, const tpl_heads *q, void *o, float *lse, void *ws, size_t ws_bytes,
-                          tpl_stream stream) {
-    PagedView view;
-    int rc = paged_view(p, kv, batch, &view);
-    if (rc != TPL_OK) return rc;
-    if (view.q_start || p->f32) return TPL_EUNSUPPORTED;
-    if (view.n_tokens == 0) return TPL_OK;
-    if (shared_len < 0 || shared_len % kv->page_size || shared_len > (int64_t)view.max_pages * kv->page_size)
-        return TPL_EINVAL;
-    PagedCall c;
-    if ((rc = paged_call(p, kv, view, q, o, lse, ws, ws_bytes, stream, &c)) != TPL_OK) return rc;
-    return shared_len == 0 ? paged_decode(c, 0, 0, 0, false) : paged_shared(c, (int)shared_len);
-}
-
 int tpl_decode_kernel_count(const tpl_plan *p, int32_t B, int32_t reduce_mode, int32_t n_layers, int32_t *count) {
     if (!p || !count || B < 1 || n_layers < 1) return TPL_EINVAL;
     if (reduce_mode != TPL_REDUCE_FUSED && reduce_mode != TPL_REDUCE_SEPARATE) return TPL_EINVAL;

@@ -8,8 +8,26 @@
 
 #include "tpl_common.cuh"
 #include "tpl_internal.h"
+#include "tpl_paged_ws.h"
 
 namespace tpl {
+
+// A kernel that needs nothing of the one before it, but of those before that, may start
+// without waiting.  Starting says nothing about memory: what it may read is passed on by
+// this word, which the kernel between sets after its own wait (its wait made the earlier
+// results visible to it, the release store passes them on to whoever acquires the word).
+// A reader that does not see it set waits instead.  A later kernel of the call, which has
+// waited for the reader, clears it.
+__device__ __forceinline__ void pdl_pass_on(unsigned *word) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(word), "r"(1u) : "memory");
+}
+__device__ __forceinline__ bool pdl_passed_on(const unsigned *word) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+    // (the copy engine's reads too)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    return v == 1u;
+}
 
 constexpr unsigned kErrPaged = 32u;  // error word: a page id, length or start out of range
 
