@@ -362,12 +362,15 @@ int tpl_prefill_chunk(tpl_plan *plan, const void *packed, const tpl_kv *kv, cons
  * one pool and one call.  A decode step is tpl_paged_append, then
  * tpl_paged_attn, between the projections tpl_qkv (on a plan without
  * TPL_ROPE; its own cache argument may be one scratch slot, S = 0) and
- * tpl_o_proj.  The pages describe neither; both follow the ownership rule of
+ * tpl_o_proj.  Those take 64 rows a call (16 with TPL_FP32_WEIGHTS), each call
+ * reading the weights, so a longer prompt's projections go in pieces; the
+ * prefill calls' projections are not to be had without their contiguous
+ * cache.  The pages describe neither; both follow the ownership rule of
  * "Tensor parallel scaling curves", "What tensor parallelism actually
  * splits": a shard's pages hold the heads it owns.
  *
- * What the device arrays say is checked by the kernels: a page id, a length
- * or a start outside its range sets the device error word
+ * What a call uses of the device arrays is checked by the kernels: a page id,
+ * a length or a start outside its range sets the device error word
  * (tpl_last_device_error returns TPL_EDEVICE), reads page 0 in its place or
  * skips the write, and never leaves the buffers; that sequence's results are
  * then not to be used. */
@@ -425,8 +428,8 @@ int tpl_paged_workspace_size(const tpl_plan *plan, int32_t n_seqs, int32_t n_tok
  * their slots, with TPL_ROPE k turned to its position first (the rotation of
  * tpl_dims), and q [n_tokens][n_q] turned the same way into q_out (q and
  * q_out both NULL: no q; q_out may be q itself, and must not overlap it
- * otherwise).  All four have the same type.  Two tokens must not share a
- * slot. */
+ * otherwise, nor k and v).  All four have the same type.  Two tokens must not
+ * share a slot. */
 int tpl_paged_append(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,
                      const tpl_heads *q_out, const tpl_heads *k, const tpl_heads *v, tpl_stream stream);
 
@@ -439,13 +442,17 @@ int tpl_paged_append(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_pag
  * does one whose every logit falls below fp32's range; such a key beside others
  * weighs nothing.  (An infinity in q, or in a key that is seen, may give NaN.)
  * Logits are q.k / sqrt(d); q is TPL_F32 or TPL_BF16 (fp32 queries cost the
- * prompts a second product).  What lies in slots that no token of the call sees
- * has no effect, whatever it is; a NaN or an infinity among the values of a key
- * that some token of a prompt (or some sequence behind a shared prefix) sees
- * may also reach the tokens that do not see it.  o, lse and the workspace
- * overlap none of the inputs.  With q_start (prompts) a plan with
- * TPL_FP32_WEIGHTS is TPL_EUNSUPPORTED, as in prefill.  The same inputs give
- * the same bits. */
+ * prompts a second product).  Roundings: every key is taken as it lies in its
+ * slot, in bf16, this call's too (tpl_decode_layer takes the newest one in
+ * fp32); fp32 queries and, for single tokens, the softmax's weights are
+ * carried in 16 bits; for prompts and behind a shared prefix the weights are
+ * bf16, off by up to 2^-8 each, as o is (tpl_prefill_layer carries 16 bits).
+ * What lies in slots that no token of the call sees has no effect, whatever it
+ * is; a NaN or an infinity among the values of a key that some token of a
+ * prompt (or some sequence behind a shared prefix) sees may also reach the
+ * tokens that do not see it.  o, lse and the workspace overlap none of the
+ * inputs.  With q_start (prompts) a plan with TPL_FP32_WEIGHTS is
+ * TPL_EUNSUPPORTED, as in prefill.  The same inputs give the same bits. */
 int tpl_paged_attn(const tpl_plan *plan, const tpl_paged_kv *kv, const tpl_paged_batch *batch, const tpl_heads *q,
                    int32_t window, int32_t sinks, void *o, float *lse, void *ws, size_t ws_bytes, tpl_stream stream);
 

@@ -4,8 +4,8 @@
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = 2^(x_j - m),  x_j = log2(e) q.k_j / sqrt(128),
 // over the keys j of the token's sequence with j < len and (j >= lo or j <
 // sinks), lo = len - window (0 without a window).  Every visible key and value
-// is read once and used by the g query heads of its kv head: at most 16
-// multiply-adds per byte, so HBM is the bound.
+// is read once and used by the g query heads of its kv head: at most 8
+// multiply-adds per byte (16 with the low parts below), so HBM is the bound.
 //
 // The work is cut at the device, because only the device knows the lengths:
 // the visible blocks of 64 keys of every (sequence, kv head) pair are laid
@@ -21,7 +21,8 @@
 // keys; it looks the pages of 32 parts up at once, a batch ahead.  Two groups
 // of four warps take alternate stages, 16 keys per warp, on mma.sync m16n8k16:
 // the queries are carried as bf16 hi + lo parts (q is fp32: together 16 bits of
-// mantissa), as is P, so the bf16 cache is the only rounding of the products.
+// mantissa), as is P: each is off by about 2^-16 of its value, far below the bf16
+// cache and a bf16 o (a plan with fp32 outputs is limited by it).
 // With g <= 8 the two parts are rows 0-7 and 8-15 of one product; with g up to
 // 16 they are two products.  tcgen05 would pad the g rows to 128.
 // At the end of a pair the eight warps leave their states in shared memory and
@@ -50,8 +51,12 @@ constexpr int kPdStage = 4 * kPdBox;              // K low and high dims, V low 
 constexpr int kPdMergeWarp = kAmWarps + 1;        // first merging warp, behind the producer
 constexpr int kPdMergeWarps = 2;
 constexpr int kPdThreads = (kPdMergeWarp + kPdMergeWarps) * 32;  // 8 consumer warps, the producer, the merging warps
-// Blocks per CTA at least: fewer make more CTAs, but more joins (5 requests of 200 keys
-// behind a prefix: 28.5, 20.8, 19.6 and 26.5 us with 1, 2, 4 and 8).
+// Blocks per CTA at least: fewer make more CTAs, but more joins.  With 1, 2, 4, 8 and 16: one
+// token at 131 keys, 8/8 heads 8.9, 10.4, 10.4, 13.0 and 11.6 us; at 518, 32/32 13.8, 13.6,
+// 12.2, 12.9 and 16.1; at 518, 64/8 13.5, 16.6, 14.8, 15.4 and 18.1; at 2001, 32/8 14.5, 12.3,
+// 11.6, 13.6 and 15.8; 5 at 201, 32/32 13.4, 13.5, 13.4, 10.2 and 14.5; 8 at 1001, 64/8 20.9,
+// 21.2, 21.3, 17.3 and 13.9; one at 8193, 64/8 23.7, 23.6, 23.6, 22.0 and 21.1.  No value is
+// best everywhere: what decides is whether the pairs end up cut.
 constexpr int kPdMinBlocks = 4;
 constexpr int kPdRow = 136;                       // floats between the rows of a state: 8 rows apart in banks
 

@@ -87,8 +87,11 @@ int paged_append(const tpl_plan *p, const tpl_paged_kv *kv, const PagedView &vie
     const bool f32 = k->type == TPL_F32;
     const int sms = num_sms_current();
     if (sms <= 0) return TPL_ECUDA;
-    // a token per CTA, or as many as fill its threads; with few tokens a token's heads
-    // are spread over more CTAs, one item per thread, so that it does not wait on one SM
+    // A token per CTA, or as many as fill its threads; with few tokens a token's heads are
+    // spread over more CTAs, one item per thread, so that it does not wait on one SM: up to 4
+    // such CTAs per SM.  Spread and not: 1 token of 64/8 heads in fp32 2.5 and 5.1 us, 32 tokens
+    // 2.7 and 5.3, 128 (9 per SM) 4.7 and 5.8, 256 8.2 and 8.8, 512 13.0 and 11.3; 32/8 in bf16,
+    // 64 tokens 2.8 and 5.1, 256 (5 per SM) 4.6 and 5.2, 512 6.6 and 5.9.
     const int items = (a.nq + 2 * view.nkv) * (f32 ? 16 : 8);
     const int parts = (items + kAppendThreads - 1) / kAppendThreads;
     const bool spread = (int64_t)view.n_tokens * parts <= 4 * sms;

@@ -26,13 +26,15 @@
 // S = Q K^T reads Q (bf16, or bf16 hi + lo when q is fp32: two products) and K
 // from shared memory; P replaces half of S in tensor memory as bf16; O += P V.
 // P has one bf16 part: with o rounded to bf16 anyway, the two roundings are of
-// the same size (2^-9 of each term against 2^-9 of the sum); the denominator
-// adds the unrounded fp32 terms.
+// the same size (up to 2^-8 of each term against up to 2^-8 of the sum); the
+// denominator adds the unrounded fp32 terms.  Against 64 bits o is off by 2.2e-3
+// of its norm, of which its own rounding is 1.7e-3.
 // The bound is the larger of the two products on the tensor cores and one
 // exponential per (row, key): 128 x 128 of them take the SM's 16 lanes of the
 // special-function unit as long as the two products take.
-// Measured: 4096 tokens after 4096 keys, 64/8 heads, bf16: 840 us (980 TFLOP/s,
-// the clock held down by the power limit; 730 us before that sets in).  S with
+// Measured: 4096 tokens after 4096 keys, 64/8 heads, bf16: 826 us (1000 TFLOP/s,
+// the clock held down by the power limit; 730 us before that sets in); with fp32
+// queries, 1.5 times the products, 950 us before that.  S with
 // N = 64 costs 48 cycles a product instead of 32 (its A operand is read from
 // shared memory each time), which the half tile in flight more than returns
 // (S of 128 keys and none in flight: 904 us).
@@ -52,10 +54,15 @@ constexpr int kPtKeys = 128;                   // keys per tile
 constexpr int kPtHalf = kPtKeys * 128;         // 128 rows x 64 dims, bf16: 16 KB
 constexpr int kPtTile = 2 * kPtHalf;           // one K, V or Q tile: 32 KB
 constexpr int kPtThreads = 384;
-// Key tiles per CTA at least.  Prompts: any (3 of 37 tokens after 900 keys: 20.8, 24.4 and
-// 26.6 us with 1, 2 and 4).  A prefix: every cut of an item is one more partial of all its
-// rows to write and join (16 sequences, 4096 keys: 36.4, 34.6, 25.2 and 28.1 us with 1, 2, 4
-// and 6; 5 sequences, 1536 keys: 19.2, 17.7, 18.4 and 21.2 us).
+// Key tiles per CTA at least.  Prompts: any.  With 1, 2 and 4: 3 of up to 37 tokens after up
+// to 900 keys 20.8, 24.4 and 26.6 us, 3 of 37 after 900 each 27.4, 23.1 and 24.5, one of 100
+// after 100 20.4, 19.1 and 27.5, 4 of 64 after 1 17.9, 24.2 and 37.9, 512 after none 29.0,
+// 28.5 and 33.9, 16 after 9000 the same.  A prefix: every cut of an item is one more partial
+// of all its rows to write and join.  With 1, 2, 4, 6 and 8 (a call, two keys of its own per
+// sequence): 5 sequences, 1536 keys, 32/32 heads 26.7, 26.8, 19.9, 21.3 and 27.8 us; 16, 4096,
+// 64/8 32.5, 32.2, 22.9, 24.0 and 25.6; 32, 2048, 40/8 32.0, 20.8, 22.2, 29.0 and 29.1; 8,
+// 1024, 16/2 17.1, 15.9, 16.8, 21.4 and 21.4; 3, 16384, 32/8 38.0, 37.9, 37.9, 38.0 and 30.2;
+// 64, 8192, 64/8 the same.
 constexpr int kPtMinTiles = 1, kPtMinTilesPrefix = 4;
 constexpr uint32_t kPtO = 0, kPtS = 256;       // TMEM columns: O of tile t at 128 t, S at 256 + 128 t
 
